@@ -312,6 +312,56 @@ W4A8_API w4a8_status w8a8_linear(const uint16_t* X, int M, int ldx, const int8_t
                                  const w4a8_wdesc* w, uint16_t* Y, int ldy, void* workspace, size_t ws_bytes,
                                  int32_t* dev_status, void* stream);
 
+/*
+ * Grouped W8A8 products: the rows of an MoE layer, sorted by expert, times
+ * their expert's INT8 weight ("Kimi 2.7 MoE, 4-bit storage to INT8" §4.4 step
+ * 4, the grouped expert GEMM, with the INT8 arithmetic above).
+ *   offsets  device int32 [E + 1]: rows [offsets[e], offsets[e+1]) belong to
+ *            expert e (w4a8_moe_dispatch or w4a8_moe_grouped_gemm's
+ *            expert_offsets_out).  An expert may have no rows.  Rows before
+ *            offsets[0] and from offsets[E] on belong to nobody: they are
+ *            neither read nor written.  Offsets that decrease or leave [0, R]
+ *            are reported as W4A8_ERR_INVALID_ARG through dev_status; nothing
+ *            outside [0, R) is accessed.
+ *   q_w      int8 [E][N][K], s_w fp32 [E][N]: E stacked w8a8_pack_weights
+ *            results; w describes one of them.
+ *   Y[r,n] = s_x[r] * (s_w[e,n] * sum_k q_x[r,k] q_w[e,n,k])   (bf16 output)
+ * The int32 sums are exact, so a row's result depends neither on the other
+ * rows nor on how the work is split: it equals w8a8_gemm's on that expert.
+ * Limits: E <= 512, R <= 2^24, K % 128 == 0, K <= 2^17, N % 16 == 0.
+ */
+
+/* Workspace bytes w8a8_grouped_gemm needs for R rows (0 when none). */
+W4A8_API size_t w8a8_grouped_workspace_size(int R, int E, const w4a8_wdesc* w);
+
+/* w8a8_grouped_gemm — the grouped product of quantized rows.
+ * qx        device int8 [R][K], 16-byte aligned; s_x device fp32 [R].
+ * Y         device bf16 [R][ldy], ldy >= N.
+ * workspace device scratch, 16-byte aligned, at least
+ *           w8a8_grouped_workspace_size(R, E, w) bytes; needs no
+ *           initialisation.  No CTA waits for another, so nothing here depends
+ *           on the grid being resident.  Calls that can overlap on the GPU
+ *           need separate workspaces; after a launch that ended with
+ *           W4A8_ERR_TIMEOUT, zero the workspace before replaying a captured
+ *           graph of it.
+ * Errors: INVALID_ARG, FORMAT_MISMATCH, UNSUPPORTED_SHAPE, WORKSPACE, CUDA;
+ *         INVALID_ARG (offsets) and TIMEOUT via dev_status. */
+W4A8_API w4a8_status w8a8_grouped_gemm(const int8_t* qx, const float* s_x, const int32_t* offsets, int R, int E,
+                                       const int8_t* q_w, const float* s_w, const w4a8_wdesc* w, uint16_t* Y, int ldy,
+                                       void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Workspace bytes w8a8_grouped_linear needs (q_x, s_x, the product's). */
+W4A8_API size_t w8a8_grouped_linear_workspace_size(int R, int E, const w4a8_wdesc* w);
+
+/* w8a8_grouped_linear — per-token INT8 quantization of X bf16 [R][ldx] (as
+ * w4a8_quant_act; X 16-byte aligned, ldx % 8 == 0) followed by
+ * w8a8_grouped_gemm, in one call.  Rows that belong to nobody are not
+ * quantized, so they may hold anything, NaN included. */
+W4A8_API w4a8_status w8a8_grouped_linear(const uint16_t* X, int R, int ldx, const int32_t* offsets, int E,
+                                         const int8_t* q_w, const float* s_w, const w4a8_wdesc* w, uint16_t* Y,
+                                         int ldy, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                         void* stream);
+
 /* ------------------------------------------------------------ W4A16 ---- */
 
 /*
@@ -467,11 +517,57 @@ W4A8_API w4a8_status w4a8_moe_experts(const uint16_t* X, const int32_t* expert_i
                                       const uint8_t* w2_z, const w4a8_wdesc* w2, uint16_t* y_out, void* workspace,
                                       size_t ws_bytes, int32_t* dev_status, void* stream);
 
+/* Workspace bytes w4a8_moe_dispatch needs for P pairs. */
+W4A8_API size_t w4a8_moe_dispatch_workspace_size(int P, int E);
+
+/* w4a8_moe_dispatch — step 2 alone: the order of P rows by expert, stable, for
+ * the grouped products.  expert_ids device int32 [P] in [0, E) (others are
+ * reported as W4A8_ERR_INVALID_ARG through dev_status and taken as 0);
+ * offsets_out int32 [E+1]; perm_out int32 [P]: position -> row; inv_out int32
+ * [P]: row -> position.  E <= 512, P <= 2^26. */
+W4A8_API w4a8_status w4a8_moe_dispatch(const int32_t* expert_ids, int P, int E, int32_t* offsets_out,
+                                       int32_t* perm_out, int32_t* inv_out, void* workspace, size_t ws_bytes,
+                                       int32_t* dev_status, void* stream);
+
 /* w4a8_moe_combine — step 7 alone: out[t] = sum_j topk_w[t,j] * y_rows[t*topk
  * + j] in fp32, slot order, one bf16 rounding (y_rows bf16 [T*topk][H] in
  * (token, slot) order; H % 8 == 0; y_rows and out 16-byte aligned). */
 W4A8_API w4a8_status w4a8_moe_combine(const uint16_t* y_rows, const float* topk_w, int T, int topk, int H,
                                       uint16_t* out, void* stream);
+
+/* ------------------------------------------------- MoE with INT8 experts -- */
+
+/*
+ * The MoE layer with W8A8 experts: w4a8_moe_grouped_gemm's seven steps with
+ * INT8 expert weights (one scale for each output channel) in steps 4 and 6:
+ *   gate_up  y = s_x (s_w acc), h = silu(gate) * up in fp32, stored as bf16;
+ *   down     y = s_h (s_w acc), expert outputs stored as bf16.
+ * w1_q int8 [E][2I][H], w1_s fp32 [E][2I] (gate = columns [0, I)); w2_q int8
+ * [E][H][I], w2_s fp32 [E][H]: stacked w8a8_pack_weights results, w1 = {K = H,
+ * N = 2I}, w2 = {K = I, N = H}.  Routing, dispatch, quantization, combine,
+ * outputs and dev_status as for w4a8_moe_grouped_gemm.
+ * Limits: E <= 512, topk <= 16 and topk <= E, H and I multiples of 128 and
+ * <= 8192, T * topk <= 2^24.
+ */
+
+/* Workspace bytes w8a8_moe_grouped_gemm needs. */
+W4A8_API size_t w8a8_moe_workspace_size(int T, int E, int topk, const w4a8_wdesc* w1, const w4a8_wdesc* w2);
+
+W4A8_API w4a8_status w8a8_moe_grouped_gemm(const uint16_t* X, const float* logits, int T, int E, int topk,
+                                           const int8_t* w1_q, const float* w1_s, const w4a8_wdesc* w1,
+                                           const int8_t* w2_q, const float* w2_s, const w4a8_wdesc* w2, uint16_t* out,
+                                           int32_t* topk_idx_out, float* topk_w_out, int32_t* expert_offsets_out,
+                                           void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* Workspace bytes w8a8_moe_experts needs for R rows. */
+W4A8_API size_t w8a8_moe_experts_workspace_size(int R, int E, const w4a8_wdesc* w1, const w4a8_wdesc* w2);
+
+/* w8a8_moe_experts — w4a8_moe_experts with INT8 experts: row r of X through
+ * expert expert_ids[r], unweighted. */
+W4A8_API w4a8_status w8a8_moe_experts(const uint16_t* X, const int32_t* expert_ids, int R, int E, const int8_t* w1_q,
+                                      const float* w1_s, const w4a8_wdesc* w1, const int8_t* w2_q, const float* w2_s,
+                                      const w4a8_wdesc* w2, uint16_t* y_out, void* workspace, size_t ws_bytes,
+                                      int32_t* dev_status, void* stream);
 
 /* --------------------------------------------------------------- status -- */
 

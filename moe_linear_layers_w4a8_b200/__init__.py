@@ -25,6 +25,9 @@ __all__ = [
     "STATUS", "PackedW8", "w8a8_pack_weights", "w8a8_gemm", "w8a8_gemm_workspace_size", "w8a8_linear",
     "w8a8_linear_workspace_size", "w4a8_moe_route", "w4a8_moe_experts", "w4a8_moe_combine",
     "w4a16_gemm", "w4a16_gemm_workspace_size",
+    "w8a8_pack_expert_weights", "w8a8_grouped_gemm", "w8a8_grouped_workspace_size", "w8a8_grouped_linear",
+    "w8a8_grouped_linear_workspace_size", "w8a8_moe_grouped_gemm", "w8a8_moe_workspace_size", "w8a8_moe_experts",
+    "w4a8_moe_dispatch",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -148,6 +151,27 @@ def load_library():
         L.w4a16_gemm_workspace_size.argtypes = [I, ctypes.POINTER(WDesc)]
         L.w4a16_gemm.restype = st
         L.w4a16_gemm.argtypes = [P, I, I, P, P, P, ctypes.POINTER(WDesc), P, I, P, S, P, P]
+        D = ctypes.POINTER(WDesc)
+        L.w8a8_grouped_workspace_size.restype = S
+        L.w8a8_grouped_workspace_size.argtypes = [I, I, D]
+        L.w8a8_grouped_gemm.restype = st
+        L.w8a8_grouped_gemm.argtypes = [P, P, P, I, I, P, P, D, P, I, P, S, P, P]
+        L.w8a8_grouped_linear_workspace_size.restype = S
+        L.w8a8_grouped_linear_workspace_size.argtypes = [I, I, D]
+        L.w8a8_grouped_linear.restype = st
+        L.w8a8_grouped_linear.argtypes = [P, I, I, P, I, P, P, D, P, I, P, S, P, P]
+        L.w8a8_moe_workspace_size.restype = S
+        L.w8a8_moe_workspace_size.argtypes = [I, I, I, D, D]
+        L.w8a8_moe_grouped_gemm.restype = st
+        L.w8a8_moe_grouped_gemm.argtypes = [P, P, I, I, I, P, P, D, P, P, D, P, P, P, P, P, S, P, P]
+        L.w8a8_moe_experts_workspace_size.restype = S
+        L.w8a8_moe_experts_workspace_size.argtypes = [I, I, D, D]
+        L.w8a8_moe_experts.restype = st
+        L.w8a8_moe_experts.argtypes = [P, P, I, I, P, P, D, P, P, D, P, P, S, P, P]
+        L.w4a8_moe_dispatch_workspace_size.restype = S
+        L.w4a8_moe_dispatch_workspace_size.argtypes = [I, I]
+        L.w4a8_moe_dispatch.restype = st
+        L.w4a8_moe_dispatch.argtypes = [P, I, I, P, P, P, P, S, P, P]
         L.w4a8_get_device_status.restype = st
         L.w4a8_get_device_status.argtypes = [P, P]
         L.w4a8_selftest_bounded_wait.restype = st
@@ -416,10 +440,12 @@ def w4a8_selftest_bounded_wait(status: torch.Tensor, limit_ns: int = 1_000_000) 
 
 @dataclasses.dataclass
 class PackedW8:
-    """Per-channel INT8 weight of the W8A8 path: q_w int8 [N, K], s_w fp32 [N]."""
+    """Per-channel INT8 weight of the W8A8 path: q_w int8 [N, K], s_w fp32 [N]
+    (or E stacked expert matrices, [E, N, K] and [E, N])."""
     q_w: torch.Tensor
     s_w: torch.Tensor
     desc: WDesc
+    experts: int = 0               # 0 = single matrix
 
     @property
     def K(self):
@@ -430,20 +456,45 @@ class PackedW8:
         return self.desc.N
 
 
-def w8a8_pack_weights(W: torch.Tensor, status: Optional[torch.Tensor] = None) -> PackedW8:
-    """Per-channel INT8 quantization of W fp32 [K, N] (device)."""
+def w8a8_pack_weights(W: torch.Tensor, status: Optional[torch.Tensor] = None, out: Optional[PackedW8] = None,
+                      expert: Optional[int] = None) -> PackedW8:
+    """Per-channel INT8 quantization of W fp32 [K, N] (device).
+    With `out` and `expert`, writes expert slot `expert` of a stacked weight."""
     L = load_library()
     _need_cuda(W)
     if W.dtype != torch.float32 or W.dim() != 2:
         raise W4A8Error(1, "W must be fp32 [K, N]")
     W = W.contiguous()
     K, N = W.shape
-    q = torch.empty(N, K, dtype=torch.int8, device=W.device)
-    s = torch.empty(N, dtype=torch.float32, device=W.device)
+    if out is None:
+        q = torch.empty(N, K, dtype=torch.int8, device=W.device)
+        s = torch.empty(N, dtype=torch.float32, device=W.device)
+    else:
+        e = int(expert)
+        if not 0 <= e < out.experts or (out.K, out.N) != (K, N):
+            raise W4A8Error(1, "w8a8_pack_weights: no such slot in the stacked weight, or another shape")
+        q, s = out.q_w[e], out.s_w[e]
     d = WDesc()
     _check(L.w8a8_pack_weights(_p(W), K, N, _p(q), _p(s), ctypes.byref(d), _p(status), _stream(W.device)),
            "w8a8_pack_weights")
-    return PackedW8(q_w=q, s_w=s, desc=d)
+    return out if out is not None else PackedW8(q_w=q, s_w=s, desc=d)
+
+
+def w8a8_pack_expert_weights(make_weight, E: int, K: int, N: int, device,
+                             status: Optional[torch.Tensor] = None) -> PackedW8:
+    """Quantizes E expert matrices (make_weight(e) -> fp32 [K, N] on `device`)
+    into one stacked PackedW8."""
+    pw = PackedW8(q_w=torch.empty(E, N, K, dtype=torch.int8, device=device),
+                  s_w=torch.empty(E, N, dtype=torch.float32, device=device),
+                  desc=WDesc(8, 1, K, K, N, LAYOUT_VERSION), experts=E)
+    for e in range(E):
+        w8a8_pack_weights(make_weight(e), status=status, out=pw, expert=e)
+    return pw
+
+
+def _need_single(w, where):
+    if w.experts:
+        raise W4A8Error(1, f"{where} takes one weight matrix, not stacked experts")
 
 
 def w8a8_gemm_workspace_size(M: int, w: PackedW8) -> int:
@@ -455,6 +506,7 @@ def w8a8_gemm(qx: torch.Tensor, s_x: torch.Tensor, w: PackedW8, out: Optional[to
     """Y bf16 [M, N] = W8A8(qx, w)."""
     L = load_library()
     _need_cuda(qx, s_x)
+    _need_single(w, "w8a8_gemm")
     if qx.dtype != torch.int8 or qx.dim() != 2 or not qx.is_contiguous():
         raise W4A8Error(1, "qx must be contiguous int8 [M, K]")
     M = qx.shape[0]
@@ -477,6 +529,7 @@ def w8a8_linear(X: torch.Tensor, w: PackedW8, out=None, workspace=None, status=N
     """Y bf16 [M, N] = the W8A8 Linear layer on X bf16 [M, K] (quantization + GEMM)."""
     L = load_library()
     _need_cuda(X)
+    _need_single(w, "w8a8_linear")
     if X.dtype != torch.bfloat16 or X.dim() != 2 or X.stride(1) != 1:
         raise W4A8Error(1, "X must be bf16 [M, K] with unit column stride")
     M = X.shape[0]
@@ -571,4 +624,213 @@ def w4a8_moe_combine(y_rows: torch.Tensor, topk_w: torch.Tensor, out: Optional[t
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=y_rows.device)
     _check(L.w4a8_moe_combine(_p(y_rows), _p(topk_w), T, k, H, _p(out), _stream(y_rows.device)), "w4a8_moe_combine")
+    return out
+
+
+def w4a8_moe_dispatch(expert_ids: torch.Tensor, E: int, status: Optional[torch.Tensor] = None):
+    """(offsets int32 [E + 1], perm int32 [P], inv int32 [P]) of expert_ids int32
+    (P elements in any shape): the stable order of the rows by expert, as the
+    grouped products take them.  perm[position] = row, inv[row] = position."""
+    L = load_library()
+    _need_cuda(expert_ids)
+    dev = expert_ids.device
+    ids = expert_ids.to(torch.int32).contiguous()
+    P = ids.numel()
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    perm = torch.empty(P, dtype=torch.int32, device=dev)
+    inv = torch.empty(P, dtype=torch.int32, device=dev)
+    need = int(L.w4a8_moe_dispatch_workspace_size(P, E))
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    _launch(dev, "w4a8_moe_dispatch", L.w4a8_moe_dispatch, ids.data_ptr(), P, int(E), offsets.data_ptr(),
+            perm.data_ptr(), inv.data_ptr(), ws.data_ptr(), ws.numel(), _addr(status))
+    return offsets, perm, inv
+
+
+# -------------------------------------------------------- grouped products --
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(dev: torch.device, where: str, fn, *args):
+    """One library call on the current stream of `dev`, with `dev` current."""
+    if torch.cuda.current_device() == dev.index:
+        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if code != 0:
+        raise W4A8Error(code, where)
+
+
+def _arg(ok: bool, what: str):
+    if not ok:
+        raise W4A8Error(1, what)
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, dev: torch.device):
+    """(address, bytes) of a scratch buffer of at least `need` bytes, and the tensor that owns it."""
+    if workspace is not None and workspace.device == dev and workspace.is_contiguous():
+        have = workspace.numel() * workspace.element_size()
+        if have >= need:
+            return workspace.data_ptr(), have, workspace
+    if need == 0:
+        return None, 0, None
+    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace.data_ptr(), need, workspace
+
+
+def _check_grouped(where: str, x, offsets, w, out, status):
+    """The shape and device rules every grouped product shares; returns (R, K, out)."""
+    _arg(x.is_cuda and x.dim() == 2, f"{where}: rows must be a CUDA matrix [R, K]")
+    dev = x.device
+    E = w.experts
+    _arg(E > 0, f"{where} takes stacked expert weights")
+    R, K = x.shape
+    _arg(K == w.desc.K, f"{where}: rows have {K} columns, the weight {w.desc.K} rows")
+    _arg(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.numel() == E + 1 and offsets.is_contiguous()
+         and offsets.device == dev, f"{where}: offsets must be contiguous int32 [E + 1] on {dev}")
+    if out is None:
+        out = torch.empty(R, w.desc.N, dtype=torch.bfloat16, device=dev)
+    else:
+        _arg(out.dtype == torch.bfloat16 and out.shape == (R, w.desc.N) and out.device == dev
+             and (out.stride(1) == 1 or w.desc.N == 1) and (out.stride(0) >= w.desc.N or R <= 1),
+             f"{where}: out must be bf16 [R, N] with unit column stride on {dev}")
+    _arg(status is None or (status.dtype == torch.int32 and status.device == dev),
+         f"{where}: status must be int32 on {dev}")
+    return R, K, out
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Row pitch of a matrix with unit column stride (a one-row matrix may carry any stride)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _check_w8(where: str, w: PackedW8, dev):
+    E, d = w.experts, w.desc
+    _arg(w.q_w.dtype == torch.int8 and tuple(w.q_w.shape) == (E, d.N, d.K) and w.q_w.is_contiguous()
+         and w.q_w.device == dev, f"{where}: q_w must be contiguous int8 [E, N, K] on {dev}")
+    _arg(w.s_w.dtype == torch.float32 and tuple(w.s_w.shape) == (E, d.N) and w.s_w.is_contiguous()
+         and w.s_w.device == dev, f"{where}: s_w must be contiguous fp32 [E, N] on {dev}")
+
+
+def w8a8_grouped_workspace_size(R: int, w: PackedW8) -> int:
+    return int(load_library().w8a8_grouped_workspace_size(int(R), w.experts, ctypes.byref(w.desc)))
+
+
+def w8a8_grouped_gemm(qx: torch.Tensor, s_x: torch.Tensor, offsets: torch.Tensor, w: PackedW8,
+                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y bf16 [R, N]: rows [offsets[e], offsets[e + 1]) of qx int8 [R, K] (scales
+    s_x fp32 [R]) times expert e of the stacked weight w.  offsets int32
+    [E + 1] stays on the device.  Rows that belong to no expert are left as
+    they are in `out` (uninitialised when `out` is not given)."""
+    L = load_library()
+    R, _, out = _check_grouped("w8a8_grouped_gemm", qx, offsets, w, out, status)
+    dev = qx.device
+    _arg(qx.dtype == torch.int8 and qx.is_contiguous(), "w8a8_grouped_gemm: qx must be contiguous int8 [R, K]")
+    _arg(s_x.dtype == torch.float32 and s_x.numel() == R and s_x.is_contiguous() and s_x.device == dev,
+         f"w8a8_grouped_gemm: s_x must be contiguous fp32 [R] on {dev}")
+    _check_w8("w8a8_grouped_gemm", w, dev)
+    d = ctypes.byref(w.desc)
+    ws, ws_bytes, _keep = _scratch(workspace, L.w8a8_grouped_workspace_size(R, w.experts, d), dev)
+    _launch(dev, "w8a8_grouped_gemm", L.w8a8_grouped_gemm, qx.data_ptr(), s_x.data_ptr(), offsets.data_ptr(), R,
+            w.experts, w.q_w.data_ptr(), w.s_w.data_ptr(), d, out.data_ptr(), _row_stride(out), ws, ws_bytes,
+            _addr(status))
+    return out
+
+
+def w8a8_grouped_linear_workspace_size(R: int, w: PackedW8) -> int:
+    return int(load_library().w8a8_grouped_linear_workspace_size(int(R), w.experts, ctypes.byref(w.desc)))
+
+
+def w8a8_grouped_linear(X: torch.Tensor, offsets: torch.Tensor, w: PackedW8, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """w8a8_grouped_gemm on X bf16 [R, K] (unit column stride): per-token INT8
+    quantization, then the grouped product, in one library call.  Rows that
+    belong to no expert are not read."""
+    L = load_library()
+    R, _, out = _check_grouped("w8a8_grouped_linear", X, offsets, w, out, status)
+    dev = X.device
+    _arg(X.dtype == torch.bfloat16 and X.stride(1) == 1,
+         "w8a8_grouped_linear: X must be bf16 [R, K] with unit column stride")
+    _check_w8("w8a8_grouped_linear", w, dev)
+    d = ctypes.byref(w.desc)
+    ws, ws_bytes, _keep = _scratch(workspace, L.w8a8_grouped_linear_workspace_size(R, w.experts, d), dev)
+    _launch(dev, "w8a8_grouped_linear", L.w8a8_grouped_linear, X.data_ptr(), R, _row_stride(X), offsets.data_ptr(),
+            w.experts, w.q_w.data_ptr(), w.s_w.data_ptr(), d, out.data_ptr(), _row_stride(out), ws, ws_bytes,
+            _addr(status))
+    return out
+
+
+# ------------------------------------------------- MoE with INT8 experts ---
+
+def w8a8_moe_workspace_size(T: int, E: int, topk: int, w1: PackedW8, w2: PackedW8) -> int:
+    return int(load_library().w8a8_moe_workspace_size(T, E, topk, ctypes.byref(w1.desc), ctypes.byref(w2.desc)))
+
+
+def w8a8_moe_grouped_gemm(X: torch.Tensor, logits: torch.Tensor, topk: int, w1: PackedW8, w2: PackedW8,
+                          workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None):
+    """One MoE expert layer with INT8 experts (route, dispatch, gate_up + SiLU*up,
+    down, combine): w1 stacks [H, 2I], w2 stacks [I, H].
+    Returns dict(out, topk_idx, topk_w, expert_offsets, workspace)."""
+    L = load_library()
+    where = "w8a8_moe_grouped_gemm"
+    _arg(X.is_cuda and X.dim() == 2 and logits.dim() == 2 and X.dtype == torch.bfloat16
+         and logits.dtype == torch.float32 and logits.device == X.device and logits.shape[0] == X.shape[0],
+         f"{where}: X must be bf16 [T, H] and logits fp32 [T, E] on one CUDA device")
+    dev = X.device
+    T, H = X.shape
+    E, topk = logits.shape[1], int(topk)
+    _arg(w1.experts == E and w2.experts == E and w1.desc.K == H, f"{where}: w1 and w2 must stack E experts for H")
+    _check_w8(where, w1, dev)
+    _check_w8(where, w2, dev)
+    _arg(status is None or (status.dtype == torch.int32 and status.device == dev),
+         f"{where}: status must be int32 on {dev}")
+    X, logits = X.contiguous(), logits.contiguous()
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    else:
+        _arg(out.dtype == torch.bfloat16 and out.shape == (T, H) and out.is_contiguous() and out.device == dev,
+             f"{where}: out must be contiguous bf16 [T, H] on {dev}")
+    idx = torch.empty(T, max(topk, 0), dtype=torch.int32, device=dev)
+    pw = torch.empty(T, max(topk, 0), dtype=torch.float32, device=dev)
+    offs = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    if T == 0:
+        offs.zero_()
+    d1, d2 = ctypes.byref(w1.desc), ctypes.byref(w2.desc)
+    ws, ws_bytes, workspace = _scratch(workspace, L.w8a8_moe_workspace_size(T, E, topk, d1, d2), dev)
+    _launch(dev, where, L.w8a8_moe_grouped_gemm, X.data_ptr(), logits.data_ptr(), T, E, topk, w1.q_w.data_ptr(),
+            w1.s_w.data_ptr(), d1, w2.q_w.data_ptr(), w2.s_w.data_ptr(), d2, out.data_ptr(), idx.data_ptr(),
+            pw.data_ptr(), offs.data_ptr(), ws, ws_bytes, _addr(status))
+    return dict(out=out, topk_idx=idx, topk_w=pw, expert_offsets=offs, workspace=workspace)
+
+
+def w8a8_moe_experts(X: torch.Tensor, expert_ids: torch.Tensor, w1: PackedW8, w2: PackedW8,
+                     workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y bf16 [R, H]: row r of X bf16 [R, H] through INT8 expert expert_ids[r] (unweighted)."""
+    L = load_library()
+    where = "w8a8_moe_experts"
+    _arg(X.is_cuda and X.dim() == 2 and X.dtype == torch.bfloat16, f"{where}: X must be bf16 [R, H] on a CUDA device")
+    dev = X.device
+    R, H = X.shape
+    E = w1.experts
+    _arg(expert_ids.device == dev and expert_ids.numel() == R and not expert_ids.dtype.is_floating_point,
+         f"{where}: expert_ids must be R integers on {dev}")
+    _arg(E > 0 and w2.experts == E and w1.desc.K == H, f"{where}: w1 and w2 must stack the same experts for H")
+    _check_w8(where, w1, dev)
+    _check_w8(where, w2, dev)
+    X, ids = X.contiguous(), expert_ids.to(torch.int32).contiguous()
+    if out is None:
+        out = torch.empty(R, H, dtype=torch.bfloat16, device=dev)
+    else:
+        _arg(out.dtype == torch.bfloat16 and out.shape == (R, H) and out.is_contiguous() and out.device == dev,
+             f"{where}: out must be contiguous bf16 [R, H] on {dev}")
+    d1, d2 = ctypes.byref(w1.desc), ctypes.byref(w2.desc)
+    ws, ws_bytes, _keep = _scratch(workspace, L.w8a8_moe_experts_workspace_size(R, E, d1, d2), dev)
+    _launch(dev, where, L.w8a8_moe_experts, X.data_ptr(), ids.data_ptr(), R, E, w1.q_w.data_ptr(), w1.s_w.data_ptr(),
+            d1, w2.q_w.data_ptr(), w2.s_w.data_ptr(), d2, out.data_ptr(), ws, ws_bytes, _addr(status))
     return out

@@ -1,0 +1,516 @@
+// Grouped W8A8 GEMM on the sm_100a tensor cores: rows sorted by expert, each
+// run of rows times its expert's INT8 weight ("Kimi 2.7 MoE, 4-bit storage to
+// INT8" §4.4 step 4 with the INT8 x INT8 product of "Inference Quantization
+// ch.1" §4 and the scales of §8.2-8.3):
+//   acc[r,n] = sum_k q_x[r,k] q_w[e,n,k]        e = expert of row r, exact int32
+//   y[r,n]   = s_x[r] * (s_w[e,n] * acc[r,n])   fp32, one bf16 rounding
+// and, for the gate_up product (columns [0, I) gate, [I, 2I) up),
+//   h[r,i]   = silu(y[r,i]) * y[r,I+i]          fp32, one bf16 rounding.
+//
+// Design (B200):
+//   * Swap-AB as in the other GEMMs here: the 128 MMA rows are weight columns
+//     n, the MMA N dimension is tokens.  A tile is a PAIR of 128-column weight
+//     boxes times up to BN rows of one expert, each box with its own TMEM
+//     accumulator: 256 consecutive columns, or 128 gate columns and the same
+//     128 up columns, so that the thread that drains gate column i also holds
+//     up column i and silu(gate) * up needs no exchange.  Per 128 k a stage
+//     moves 32 KB of weights and BN * 128 bytes of rows for 2 x 128 x BN
+//     products: the traffic of a 256-wide tile at half its row granularity,
+//     which ragged groups waste less of.
+//   * One 4-D tensor map (k, column, half, expert) brings both boxes in one
+//     request; columns past the expert's last are filled with zeros instead of
+//     the next expert's weights.
+//   * Rows of a tile past its expert's last are loaded (they belong to the next
+//     expert) but neither multiplied, beyond a multiple of 16 (the MMA's N is
+//     set per tile), nor stored: every output row has one writer.
+//   * The host does not know the offsets, so every CTA derives the tile list:
+//     m-tiles per expert, their prefix sum in shared memory, tile -> (expert,
+//     n-tile, m-tile) by binary search.  m-tiles run inside n-tiles, so tiles
+//     that share a weight box run side by side.
+//   * Persistent.  Enough tiles: handed out round-robin.  Few tiles (a decode
+//     step of few experts): the (tile, k-block) units are cut into equal
+//     ranges, one for each CTA.  A CTA that holds part of a tile stores its
+//     int32 partial tile and counts itself in; the one that completes the
+//     count adds all parts and writes the output.  Integer sums are exact in
+//     any order, so results do not depend on who comes last, and no CTA ever
+//     waits for another.
+//   * Warp 0 streams weights, warp 10 rows, one lane of warp 1 issues the
+//     MMAs, warps 2-9 drain (each its own 32 columns, staged in 2 KB of shared
+//     memory of its own and written as 16-byte pieces).  Two accumulator
+//     pairs alternate, so a drain overlaps the next tile's MMAs.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
+
+namespace w4a8 {
+
+struct W8GroupedParams {
+    int N;                       // output columns (gate_up: I)
+    int K, KB;                   // KB = K / 128 k-blocks
+    int E, R;
+    int n_tiles;                 // ceil(N / 256), gate_up: ceil(I / 128)
+    const int32_t* offsets;      // [E + 1] device
+    const float* s_w;            // [E][N], gate_up: [E][2I]
+    const float* s_x;            // [R]
+    uint16_t* Y;
+    int ldy;
+    int vec16;                   // Y and ldy allow 16-byte row stores
+    int split_tiles;             // tiles below which units may be split (0: never)
+    int32_t* partial;            // [2 * grid][2][BN][128] int32 partial tiles
+    unsigned long long* counts;  // [split_tiles] arrivals of this launch
+    unsigned long long epoch;
+    int32_t* status;
+    unsigned long long wait_ns;
+};
+
+constexpr int kW8GThreads = 352;     // 2 producers, MMA, 8 epilogue warps
+constexpr int kW8GEpiWarp0 = 2;
+constexpr int kW8GXWarp = 10;
+constexpr int kGroupedMaxExperts = 512;
+
+template <int BN>
+struct W8GCfg {
+    static constexpr int A_STAGE = 256 * 128;               // two weight boxes of 128 columns x 128 k
+    static constexpr int XBOX = BN < 64 ? BN : 64;          // rows per activation request
+    static constexpr int B_STAGE = BN * 128;
+    static constexpr int STAGE = A_STAGE + B_STAGE;
+    static constexpr int STG = 8 * 2048;                    // output staging: 32 tokens x 32 columns per warp
+    static constexpr int TABLE = 3 * (kGroupedMaxExperts + 1) * 4;
+    static constexpr int NST_RAW = (227 * 1024 - 1024 - STG - TABLE - 512) / STAGE;
+    static constexpr int NST = NST_RAW > 8 ? 8 : NST_RAW;
+    static constexpr int OFF_STG = NST * STAGE;
+    static constexpr int OFF_BAR = OFF_STG + STG;
+    static constexpr int NUM_BARS = 3 * NST + 5;
+    static constexpr int OFF_TABLE = OFF_BAR + NUM_BARS * 8;
+    static constexpr int OFF_MISC = OFF_TABLE + TABLE;
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static constexpr int ACC_COLS = 4 * BN;                 // two pairs of accumulators
+    static constexpr uint32_t TMEM_COLS = ACC_COLS;
+    static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128, "BN");
+    static_assert(NST >= 3, "stages");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// 4-D tiled tensor load (coordinates innermost first).
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+// Rows and m-tiles of every expert, in shared memory.
+struct GroupTable {
+    int32_t* beg;   // [E] first row
+    int32_t* cnt;   // [E] rows
+    int32_t* mt;    // [E + 1] prefix of m-tiles
+};
+
+// Fills the table from the device offsets (all threads of the CTA; ends with
+// a barrier).  Offsets outside [0, R] or decreasing are reported and clamped,
+// so that no row index derived from them leaves [0, R).
+__device__ __forceinline__ void build_group_table(const GroupTable& g, const int32_t* offsets, int E, int R, int bn,
+                                                  int32_t* status) {
+    const int tid = threadIdx.x, nthr = blockDim.x;
+    for (int e = tid; e < E; e += nthr) {
+        const int32_t o0 = offsets[e], o1 = offsets[e + 1];
+        if ((o0 < 0) | (o1 > R) | (o1 < o0)) report_status(status, 1);
+        const int32_t a = min(max(o0, 0), R), b = min(max(o1, 0), R);
+        const int32_t c = max(b - a, 0);
+        g.beg[e] = a;
+        g.cnt[e] = c;
+        g.mt[e + 1] = (c + bn - 1) / bn;
+    }
+    __syncthreads();
+    if (tid < 32) {  // inclusive scan, one run of consecutive experts per lane
+        const int per = (E + 31) / 32;
+        const int e0 = min(tid * per, E), e1 = min(e0 + per, E);
+        int32_t sum = 0;
+        for (int e = e0; e < e1; ++e) sum += g.mt[e + 1];
+        int32_t inc = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+            if (tid >= off) inc += v;
+        }
+        int32_t run = inc - sum;
+        for (int e = e0; e < e1; ++e) {
+            run += g.mt[e + 1];
+            g.mt[e + 1] = run;
+        }
+        if (tid == 0) g.mt[0] = 0;
+    }
+    __syncthreads();
+}
+
+// A CTA's share of the work, as segments: k-blocks [kb0, kb1) of a tile.
+struct GroupedWalk {
+    long long tiles, t;          // whole tiles: next tile (strided by the grid)
+    int u, u1, Q, KB;            // split: unit range
+    bool split;
+
+    __device__ __forceinline__ GroupedWalk(const GroupTable& g, int E, int n_tiles, int KB_, int split_tiles) {
+        KB = KB_;
+        tiles = (long long)g.mt[E] * n_tiles;
+        const long long grid = gridDim.x;
+        const long long waves = (tiles + grid - 1) / grid;
+        // more than 15% of the CTAs idle in the last wave
+        split = tiles < split_tiles && KB > 1 && 20 * tiles < 17 * waves * grid;
+        t = blockIdx.x;
+        Q = 0;
+        u = u1 = 0;
+        if (split) {
+            const int U = (int)tiles * KB;  // below split_tiles * 2^10
+            Q = (U + (int)grid - 1) / (int)grid;
+            u = min((int)blockIdx.x * Q, U);
+            u1 = min(u + Q, U);
+        }
+    }
+    // next segment; false at the end
+    __device__ __forceinline__ bool next(long long& tile, int& kb0, int& kb1) {
+        if (split) {
+            if (u >= u1) return false;
+            const int ti = u / KB;
+            tile = ti;
+            kb0 = u - ti * KB;
+            kb1 = min(KB, kb0 + (u1 - u));
+            u += kb1 - kb0;
+            return true;
+        }
+        if (t >= tiles) return false;
+        tile = t;
+        kb0 = 0;
+        kb1 = KB;
+        t += gridDim.x;
+        return true;
+    }
+};
+
+struct GroupedTile {
+    int e, nt, row0, rows;
+    __device__ __forceinline__ GroupedTile(const GroupTable& g, int E, int n_tiles, int bn, long long tile) {
+        const int m = (int)(tile / n_tiles);   // in [mt[e], mt[e + 1])
+        int lo = 0, hi = E - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (g.mt[mid + 1] <= m) lo = mid + 1; else hi = mid;
+        }
+        e = lo;
+        const int m0 = g.mt[lo], mc = g.mt[lo + 1] - m0;
+        const int local = (int)(tile - (long long)m0 * n_tiles);
+        nt = local / mc;
+        const int mi = local - nt * mc;
+        row0 = g.beg[lo] + mi * bn;
+        rows = min(bn, g.cnt[lo] - mi * bn);
+    }
+};
+
+// Counts this CTA in at a tile's arrival word and returns how many were there
+// before it.  The word holds (epoch, count); any other epoch's content counts
+// as zero, so the word needs no initialisation.  The last of `n` arrivals
+// clears it, so that a replayed graph (same epoch) starts over.
+__device__ __forceinline__ int count_in(unsigned long long* word, unsigned long long epoch, int n) {
+    const unsigned long long base = epoch << 8;
+    unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(word);
+    while (true) {
+        const int before = (cur >> 8) == (base >> 8) ? (int)(cur & 0xFFu) : 0;
+        const unsigned long long want = before + 1 == n ? 0ull : base | (unsigned long long)(before + 1);
+        const unsigned long long got = atomicCAS(word, cur, want);
+        if (got == cur) return before;
+        cur = got;
+    }
+}
+
+template <int BN, bool GATEUP>
+__global__ void __launch_bounds__(kW8GThreads, 1)
+    w8a8_grouped_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                        const W8GroupedParams p) {
+    using C = W8GCfg<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* w_full = bars;                // [NST] weight boxes landed
+    uint64_t* x_full = w_full + C::NST;     // [NST] rows landed
+    uint64_t* empty = x_full + C::NST;      // [NST] their MMAs completed
+    uint64_t* acc_full = empty + C::NST;    // [2] accumulator pair's MMAs completed
+    uint64_t* acc_empty = acc_full + 2;     // [2] drained by the 8 epilogue warps
+    uint64_t* drain = acc_empty + 2;        // [1] every MMA of the CTA completed
+    GroupTable g;
+    g.beg = reinterpret_cast<int32_t*>(smem + C::OFF_TABLE);
+    g.cnt = g.beg + kGroupedMaxExperts + 1;
+    g.mt = g.cnt + kGroupedMaxExperts + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
+    int* last_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        pdl_launch_dependents();
+        for (int i = 0; i < C::NST; ++i) {
+            mbar_init(&w_full[i], 1);
+            mbar_init(&x_full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 8);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+        prefetch_tmap(&tmap_w);
+        prefetch_tmap(&tmap_x);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    // offsets and rows may come from the kernel launched just before
+    pdl_wait_prerequisites();
+    build_group_table(g, p.offsets, p.E, p.R, BN, blockIdx.x == 0 ? p.status : nullptr);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const WaitCtx wc{abort_flag, p.status, wait_cycles_for_ns(p.wait_ns)};
+    GroupedWalk walk(g, p.E, p.n_tiles, p.KB, p.split_tiles);
+    long long tile;
+    int kb0, kb1;
+
+    if (warp == 0 || warp == kW8GXWarp) {
+        // ------------------------------------------------------ producers --
+        if (lane == 0) {
+            const bool is_w = warp == 0;
+            uint64_t* full = is_w ? w_full : x_full;
+            Ring rs;
+            long long issued = 0;
+            bool ok = true;
+            while (ok && walk.next(tile, kb0, kb1)) {
+                const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
+                const int boxes = gt.rows > C::XBOX ? 2 : 1;
+                const int col = gt.nt * (GATEUP ? 128 : 256);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!wait_bounded(&empty[rs.idx], rs.phase ^ 1u, wc)) { ok = false; break; }
+                    uint8_t* st = smem + rs.idx * C::STAGE;
+                    if (is_w) {
+                        mbar_arrive_expect_tx(&full[rs.idx], C::A_STAGE);
+                        tma_load_4d(st, &tmap_w, &full[rs.idx], kb * 128, col, 0, gt.e);
+                    } else {
+                        mbar_arrive_expect_tx(&full[rs.idx], boxes * (C::XBOX * 128));
+                        st += C::A_STAGE;
+                        tma_load_2d(st, &tmap_x, &full[rs.idx], kb * 128, gt.row0);
+                        if (boxes == 2)
+                            tma_load_2d(st + C::XBOX * 128, &tmap_x, &full[rs.idx], kb * 128, gt.row0 + C::XBOX);
+                    }
+                    rs.next(C::NST);
+                    ++issued;
+                }
+            }
+            // copies in flight land before the CTA leaves
+            WaitCtx wd = wc;
+            volatile int no_abort = 0;
+            wd.abort = &no_abort;
+            Ring d = rs;
+            for (long long k = 0; k < issued && k < C::NST; ++k) {
+                ring_back(d, C::NST);
+                (void)wait_bounded(&full[d.idx], d.phase, wd);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------ MMA issue --
+        if (lane == 0) {
+            Ring rs, ra;
+            bool ok = true;
+            while (ok && walk.next(tile, kb0, kb1)) {
+                const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
+                const uint32_t idesc = idesc_i8((gt.rows + 15) & ~15);
+                const bool two = GATEUP || p.N - gt.nt * 256 > 128;
+                if (!wait_bounded(&acc_empty[ra.idx], ra.phase ^ 1u, wc)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d0 = tmem_base + ra.idx * (2 * BN);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!wait_bounded(&w_full[rs.idx], rs.phase, wc) || !wait_bounded(&x_full[rs.idx], rs.phase, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(smem + rs.idx * C::STAGE);
+                    const uint64_t adesc = umma_desc_kmajor(a_addr, 128);
+                    const uint64_t bdesc = umma_desc_kmajor(a_addr + C::A_STAGE, 128);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t acc = (kb > kb0 || kk > 0) ? 1u : 0u;
+                        mma_i8(d0, adesc + 2 * kk, bdesc + 2 * kk, idesc, acc);
+                        if (two) mma_i8(d0 + BN, adesc + (128 * 128 >> 4) + 2 * kk, bdesc + 2 * kk, idesc, acc);
+                    }
+                    tc_commit(&empty[rs.idx]);
+                    rs.next(C::NST);
+                }
+                if (!ok) break;
+                tc_commit(&acc_full[ra.idx]);
+                ra.next(2);
+            }
+            // drain: every MMA issued above completes before TMEM is freed
+            tc_commit(drain);
+            WaitCtx wd = wc;
+            volatile int no_abort = 0;
+            wd.abort = &no_abort;
+            (void)wait_bounded(drain, 0, wd);
+        }
+    } else {
+        // ------------------------------------------------------- epilogue --
+        const int q = warp & 3;                          // TMEM lane quadrant
+        const int grp = (warp - kW8GEpiWarp0) >> 2;      // plain: column half; gate_up: every other token batch
+        const uint32_t lane_addr = ((uint32_t)(q * 32)) << 16;
+        uint16_t* stg = reinterpret_cast<uint16_t*>(smem + C::OFF_STG) + (warp - kW8GEpiWarp0) * 1024;
+        // tokens per batch: a thread holds LB accumulators (gate_up: LB pairs)
+        constexpr int LB = GATEUP ? (BN < 64 ? BN / 2 : 32) : (BN < 32 ? BN : 32);
+        constexpr int STEP = GATEUP ? 2 * LB : LB;
+        const int et = threadIdx.x - kW8GEpiWarp0 * 32;  // 0..255
+        Ring ra;
+        while (walk.next(tile, kb0, kb1)) {
+            const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
+            bool ok = warp_wait_bounded(&acc_full[ra.idx], ra.phase, wc);
+            if (walk.split) ok = !named_bar_or(1, 256, !ok);  // one decision before the barriers below
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tacc = tmem_base + lane_addr + ra.idx * (2 * BN);
+            const int half = GATEUP ? 0 : grp;
+            const int c_in = q * 32 + lane;                                      // column within the 128
+            const int col0 = GATEUP ? gt.nt * 128 + q * 32 : gt.nt * 256 + half * 128 + q * 32;  // the warp's first
+            const int first = GATEUP ? grp * LB : 0;                             // the warp's first token batch
+            const bool live = col0 < p.N;                                        // warp-uniform
+            const int32_t* parts = nullptr;   // the tile's partial tiles, when this CTA adds them
+            int nparts = 0, c_first = 0;
+            bool write = live;
+            if (walk.split && (kb0 > 0 || kb1 < p.KB)) {
+                // part of a tile: the raw sums go to this CTA's slot
+                const long long tile_ints = 2LL * BN * 128;
+                int32_t* dst = p.partial + (2LL * blockIdx.x + (kb0 > 0 ? 0 : 1)) * tile_ints;
+                if (live) {
+#pragma unroll 1
+                    for (int c0 = first; c0 < gt.rows; c0 += STEP) {
+#pragma unroll
+                        for (int hh = 0; hh < (GATEUP ? 2 : 1); ++hh) {
+                            const int hf = GATEUP ? hh : half;
+                            uint32_t v[LB];
+                            tmem_ld32<LB>(tacc + hf * BN + c0, v);
+                            tmem_wait_ld();
+                            int32_t* d = dst + (hf * BN + c0) * 128 + c_in;
+#pragma unroll
+                            for (int j = 0; j < LB; ++j) d[j * 128] = (int32_t)v[j];
+                        }
+                    }
+                }
+                tc_fence_before();
+                const int t0 = (int)tile * p.KB;
+                c_first = t0 / walk.Q;
+                nparts = (t0 + p.KB - 1) / walk.Q - c_first + 1;
+                named_bar_sync(1, 256);
+                if (et == 0) {
+                    __threadfence();
+                    *last_flag = count_in(p.counts + tile, p.epoch, nparts) == nparts - 1;
+                    __threadfence();
+                }
+                named_bar_sync(1, 256);
+                write = live && *reinterpret_cast<volatile int*>(last_flag) != 0;
+                // the CTA holding the tile's first k-blocks stored to its slot 1, the others to slot 0
+                parts = p.partial;
+            }
+            if (write) {
+                const float* sw = p.s_w + (long long)gt.e * (GATEUP ? 2 * p.N : p.N);
+                const int n = col0 + lane;
+                const bool n_ok = n < p.N;
+                const float sw0 = n_ok ? __ldg(sw + n) : 0.0f;
+                const float sw1 = GATEUP && n_ok ? __ldg(sw + p.N + n) : 0.0f;
+                auto load = [&](int hf, int c0, uint32_t* v) {
+                    if (parts) {
+                        const long long tile_ints = 2LL * BN * 128;
+#pragma unroll
+                        for (int j = 0; j < LB; ++j) v[j] = 0u;
+#pragma unroll 1
+                        for (int k = 0; k < nparts; ++k) {
+                            const int c = c_first + k;
+                            const int slot = c * walk.Q > (int)tile * p.KB ? 0 : 1;
+                            const int32_t* s = parts + (2LL * c + slot) * tile_ints + (hf * BN + c0) * 128 + c_in;
+#pragma unroll
+                            for (int j = 0; j < LB; ++j) v[j] += (uint32_t)__ldcg(s + j * 128);
+                        }
+                    } else {
+                        tmem_ld32<LB>(tacc + hf * BN + c0, v);
+                    }
+                };
+#pragma unroll 1
+                for (int c0 = first; c0 < gt.rows; c0 += STEP) {
+                    uint32_t a[LB], b[GATEUP ? LB : 1];
+                    load(GATEUP ? 0 : half, c0, a);
+                    if constexpr (GATEUP) load(1, c0, b);
+                    const float sxl = lane < LB && c0 + lane < gt.rows ? __ldg(p.s_x + gt.row0 + c0 + lane) : 0.0f;
+                    if (!parts) tmem_wait_ld();
+                    __syncwarp();  // the previous batch's copy-out is done with the staging
+#pragma unroll
+                    for (int j = 0; j < LB; ++j) {
+                        const float sx = __shfl_sync(0xFFFFFFFFu, sxl, j);
+                        float y = sx * (sw0 * (float)(int32_t)a[j]);
+                        if constexpr (GATEUP) {
+                            const float up = sx * (sw1 * (float)(int32_t)b[j]);
+                            y = (y / (1.0f + expf(-y))) * up;
+                        }
+                        stg[j * 32 + lane] = f32_to_bf16_bits(y);
+                    }
+                    __syncwarp();
+                    // LB rows of 32 columns: 16-byte pieces
+#pragma unroll
+                    for (int i = lane; i < LB * 4; i += 32) {
+                        const int j = i >> 2, col = col0 + (i & 3) * 8;
+                        if (c0 + j < gt.rows && col < p.N) {
+                            const uint4 val = *reinterpret_cast<const uint4*>(stg + j * 32 + (i & 3) * 8);
+                            uint16_t* dst = p.Y + (long long)(gt.row0 + c0 + j) * p.ldy + col;
+                            if (p.vec16) {
+                                *reinterpret_cast<uint4*>(dst) = val;
+                            } else {
+                                const uint32_t w4[4] = {val.x, val.y, val.z, val.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    dst[2 * k] = (uint16_t)(w4[k] & 0xFFFFu);
+                                    dst[2 * k + 1] = (uint16_t)(w4[k] >> 16);
+                                }
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+            }
+            // the accumulator pair is free for the MMA's next tile
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[ra.idx]);
+            ra.next(2);
+        }
+    }
+
+    // ----------------------------------------------------------- teardown --
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+}
+
+// Launches the grouped W8A8 kernel for a tile of BN in {16, 32, 64, 128} rows
+// (defined in gemm_w8a8_grouped.cu).  Status codes as in w4a8.h.
+int launch_w8a8_grouped(int bn, bool gate_up, const CUtensorMap& tmap_w, const CUtensorMap& tmap_x,
+                        const W8GroupedParams& p, int grid, cudaStream_t stream);
+
+// Rows of one activation request of a tile of bn rows.
+inline int w8a8_grouped_xbox(int bn) { return bn < 64 ? bn : 64; }
+
+}  // namespace w4a8

@@ -82,11 +82,20 @@ __device__ __forceinline__ void quant_chunk8(const uint4 raw, float d, float r, 
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 256;
 
+// The rows a grouped call uses, known on the device only: [*first, *end).
+// Null pointers mean every row.  Rows outside are neither read nor written (a
+// padded batch may hold anything there).
+struct RowRange {
+    const int32_t* first;
+    const int32_t* end;
+    __device__ __forceinline__ bool has(int m) const { return first == nullptr || (m >= *first && m < *end); }
+};
+
 template <int CPT>
 __global__ void __launch_bounds__(kQuantThreads) quant_act_kernel(
     const uint16_t* __restrict__ X, int K, int ldx, int8_t* __restrict__ q, float* __restrict__ s_x,
     int32_t* __restrict__ rowsum, int group, const int32_t* __restrict__ dest, int dest_k,
-    int32_t* status) {
+    const RowRange used, int32_t* status) {
     // A GEMM launched after this kernel with programmatic stream serialization
     // may start its prologue and weight streaming now (it reads only packed
     // weights and scales before it waits for this grid's completion).
@@ -96,6 +105,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_act_kernel(
     pdl_launch_dependents();
     pdl_wait_prerequisites();
     const int m = blockIdx.x;
+    if (!used.has(m)) return;
     const int tid = threadIdx.x;
     const int nchunk = K >> 3;
     const uint4* xr = reinterpret_cast<const uint4*>(X + (size_t)m * ldx);
@@ -169,10 +179,11 @@ __global__ void __launch_bounds__(kQuantThreads) quant_act_kernel(
 // quant_act_kernel.
 __global__ void __launch_bounds__(kQuantThreads) quant_act_long_kernel(
     const uint16_t* __restrict__ X, int K, int ldx, int8_t* __restrict__ q, float* __restrict__ s_x,
-    int32_t* __restrict__ rowsum, int group, int32_t* status) {
+    int32_t* __restrict__ rowsum, int group, const RowRange used, int32_t* status) {
     pdl_launch_dependents();
     pdl_wait_prerequisites();
     const int m = blockIdx.x;
+    if (!used.has(m)) return;
     const int tid = threadIdx.x;
     const int nchunk = K >> 3;
     const uint4* xr = reinterpret_cast<const uint4*>(X + (size_t)m * ldx);
@@ -229,12 +240,13 @@ constexpr int kQuantRowsPerCta = 8;
 template <int CPL>
 __global__ void __launch_bounds__(32 * kQuantRowsPerCta) quant_act_rows_kernel(
     const uint16_t* __restrict__ X, int rows, int K, int ldx, int8_t* __restrict__ q, float* __restrict__ s_x,
-    int32_t* __restrict__ rowsum, int group, const int32_t* __restrict__ dest, int dest_k, int32_t* status) {
+    int32_t* __restrict__ rowsum, int group, const int32_t* __restrict__ dest, int dest_k, const RowRange used,
+    int32_t* status) {
     pdl_launch_dependents();
     pdl_wait_prerequisites();
     const int lane = threadIdx.x & 31;
     const int m = blockIdx.x * kQuantRowsPerCta + (threadIdx.x >> 5);
-    if (m >= rows) return;  // warp-uniform
+    if (m >= rows || !used.has(m)) return;  // warp-uniform
     const int nchunk = K >> 3;
     const uint4* xr = reinterpret_cast<const uint4*>(X + (size_t)m * ldx);
 

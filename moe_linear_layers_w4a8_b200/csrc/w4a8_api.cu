@@ -18,6 +18,7 @@
 #include "gemm_launch.cuh"
 #include "kernels_misc.cuh"
 #include "gemm_w8a8.cuh"
+#include "gemm_w8a8_grouped.cuh"
 #include "gemm_w4a16.cuh"
 
 using namespace w4a8;
@@ -265,7 +266,7 @@ w4a8_status launch_maybe_pdl(void (*kern)(KArgs...), unsigned grid, unsigned blo
 
 w4a8_status launch_quant(const uint16_t* X, int rows, int K, int ldx, int8_t* q, float* s_x, int32_t* rowsum,
                          int group, const int32_t* dest, int dest_k, int32_t* status, cudaStream_t s,
-                         bool pdl = false) {
+                         bool pdl = false, RowRange used = RowRange{nullptr, nullptr}) {
     if (rows == 0) return W4A8_OK;
     if (rows >= 8192 && K <= 1536) {
         // very many short rows (measured on B200: 24576 x 1408 80 -> 57 us;
@@ -277,7 +278,7 @@ w4a8_status launch_quant(const uint16_t* X, int rows, int K, int ldx, int8_t* q,
         const unsigned threads = 32 * kQuantRowsPerCta;
         w4a8_status st = W4A8_ERR_UNSUPPORTED_SHAPE;
         switch (cpl) {
-#define W4A8_QROWS(n) case n: st = launch_maybe_pdl(quant_act_rows_kernel<n>, blocks, threads, s, pdl, X, rows, K, ldx, q, s_x, rowsum, group, dest, dest_k, status); break;
+#define W4A8_QROWS(n) case n: st = launch_maybe_pdl(quant_act_rows_kernel<n>, blocks, threads, s, pdl, X, rows, K, ldx, q, s_x, rowsum, group, dest, dest_k, used, status); break;
             W4A8_QROWS(1) W4A8_QROWS(2) W4A8_QROWS(4) W4A8_QROWS(6) W4A8_QROWS(8) W4A8_QROWS(12) W4A8_QROWS(16)
 #undef W4A8_QROWS
         }
@@ -288,12 +289,12 @@ w4a8_status launch_quant(const uint16_t* X, int rows, int K, int ldx, int8_t* q,
         // rows longer than 8192: two passes over the row (scatter form unused here)
         if (dest) return W4A8_ERR_UNSUPPORTED_SHAPE;
         const w4a8_status st = launch_maybe_pdl(quant_act_long_kernel, (unsigned)rows, kQuantThreads, s, pdl, X, K,
-                                                ldx, q, s_x, rowsum, group, status);
+                                                ldx, q, s_x, rowsum, group, used, status);
         return st != W4A8_OK ? st : last_cuda();
     }
     w4a8_status st = W4A8_ERR_UNSUPPORTED_SHAPE;
     switch (cpt) {
-#define W4A8_QCTA(n) case n: st = launch_maybe_pdl(quant_act_kernel<n>, (unsigned)rows, kQuantThreads, s, pdl, X, K, ldx, q, s_x, rowsum, group, dest, dest_k, status); break;
+#define W4A8_QCTA(n) case n: st = launch_maybe_pdl(quant_act_kernel<n>, (unsigned)rows, kQuantThreads, s, pdl, X, K, ldx, q, s_x, rowsum, group, dest, dest_k, used, status); break;
         W4A8_QCTA(1) W4A8_QCTA(2) W4A8_QCTA(3) W4A8_QCTA(4)
 #undef W4A8_QCTA
         default: return W4A8_ERR_UNSUPPORTED_SHAPE;
@@ -334,6 +335,39 @@ MoeLayout moe_layout(int T, int E, int topk, int H, int I) {
     L.dcnt = o;      o = align_up(o + sizeof(int32_t) * (size_t)dispatch_ctas(T) * E, 256);
     L.total = o;
     return L;
+}
+
+w4a8_status launch_route(const float* logits, int T, int E, int topk, int32_t* idx, float* w, int32_t* status,
+                         cudaStream_t s) {
+    const int epl = (E + 31) / 32;
+    const unsigned blocks = (unsigned)(((long long)T * 32 + 255) / 256);
+    switch (epl) {
+#define W4A8_ROUTE(n) case n: route_topk_kernel<n><<<blocks, 256, 0, s>>>(logits, T, E, topk, idx, w, status); break;
+        W4A8_ROUTE(1) W4A8_ROUTE(2) W4A8_ROUTE(3) W4A8_ROUTE(4) W4A8_ROUTE(5) W4A8_ROUTE(6) W4A8_ROUTE(7)
+        W4A8_ROUTE(8) W4A8_ROUTE(9) W4A8_ROUTE(10) W4A8_ROUTE(11) W4A8_ROUTE(12) W4A8_ROUTE(13)
+        W4A8_ROUTE(14) W4A8_ROUTE(15) W4A8_ROUTE(16)
+#undef W4A8_ROUTE
+        default: return W4A8_ERR_UNSUPPORTED_SHAPE;
+    }
+    return last_cuda();
+}
+
+// Expert offsets, m-tile prefix for tiles of bn rows, and the permutation of
+// T * topk pairs, all ids already in [0, E).  dcnt: dispatch_ctas(T) * E ints.
+w4a8_status launch_dispatch(const int32_t* idx, int T, int E, int topk, int bn, int32_t* offsets, int32_t* mtile_off,
+                            int32_t* perm, int32_t* inv, int32_t* dcnt, cudaStream_t s) {
+    if (T <= kDispatchThreads) {
+        dispatch_kernel<<<1, kDispatchThreads, 0, s>>>(idx, T, E, topk, bn, offsets, mtile_off, perm, inv);
+        return last_cuda();
+    }
+    const int tpc = dispatch_tokens_per_cta(T), C = dispatch_ctas(T);
+    dispatch_count_kernel<<<C, kDispatchThreads, 0, s>>>(idx, T, E, topk, tpc, dcnt);
+    w4a8_status st = last_cuda();
+    if (st != W4A8_OK) return st;
+    dispatch_scan_kernel<<<1, kDispatchScanThreads, 0, s>>>(dcnt, C, E, bn, offsets, mtile_off);
+    if ((st = last_cuda()) != W4A8_OK) return st;
+    dispatch_scatter_kernel<<<C, kDispatchThreads, 0, s>>>(idx, T, E, topk, tpc, dcnt, perm, inv);
+    return last_cuda();
 }
 
 w4a8_status check_moe(int T, int E, int topk, const w4a8_wdesc* w1, const w4a8_wdesc* w2) {
@@ -451,6 +485,120 @@ w4a8_status w8_gemm_impl(const int8_t* qx, const float* s_x, const int8_t* q_w, 
     p.wait_ns = kDefaultWaitNs;
     return static_cast<w4a8_status>(
         launch_w8a8(pl.bn, pl.split, tw, tx, p, pl.grid, static_cast<cudaStream_t>(stream)));
+}
+
+// Launch plan of a grouped W8A8 GEMM over R rows and E experts: N output
+// columns (gate_up: I).  The rows of each expert are known on the device only,
+// so the plan fixes the tile height, whether units may be split (not when R
+// rows make four tiles for each CTA at the least) and the workspace for it.
+struct W8GroupedPlan {
+    int bn, n_tiles, KB, grid, split_tiles;
+    size_t counts_off, ws_bytes;
+};
+
+W8GroupedPlan plan_w8_grouped(long long R, int E, int N, int K, bool gate_up, int sms) {
+    W8GroupedPlan pl{};
+    pl.bn = pick_bn((R + E - 1) / E);
+    const int cols = gate_up ? 128 : 256;
+    pl.n_tiles = (N + cols - 1) / cols;
+    pl.KB = K / 128;
+    pl.grid = sms <= 0 ? 1 : (sms > 254 ? 254 : sms);  // arrivals are counted in 8 bits
+    const long long fewest = ((R + pl.bn - 1) / pl.bn) * pl.n_tiles;
+    if (pl.KB > 1 && fewest < 4LL * pl.grid) {
+        pl.split_tiles = 4 * pl.grid;
+        pl.counts_off = (size_t)2 * pl.grid * 2 * pl.bn * 128 * sizeof(int32_t);
+        pl.ws_bytes = pl.counts_off + (size_t)pl.split_tiles * sizeof(unsigned long long);
+    }
+    return pl;
+}
+
+// 4-D tensor map over the stacked INT8 weights q_w [E][N_all][K], seen as
+// (k, column, half, expert): gate_up has two halves of I columns, read as a
+// box of 128 columns of each; the plain product reads 256 columns of one.
+bool make_w8_grouped_tmap(CUtensorMap* map, const void* base, int E, int N, int K, bool gate_up) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    const cuuint64_t halves = gate_up ? 2 : 1, half = (cuuint64_t)N * K;
+    cuuint64_t dims[4] = {(cuuint64_t)K, (cuuint64_t)N, halves, (cuuint64_t)E};
+    cuuint64_t strides[3] = {(cuuint64_t)K, half, halves * half};
+    cuuint32_t box[4] = {128, gate_up ? 128u : 256u, gate_up ? 2u : 1u, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// The grouped product (gate_up: with silu(gate) * up).  N: output columns.
+w4a8_status launch_w8_grouped(const int8_t* qx, const float* s_x, const int32_t* offsets, int R, int E,
+                              const int8_t* q_w, const float* s_w, int N, int K, bool gate_up, uint16_t* Y, int ldy,
+                              void* workspace, int32_t* dev_status, cudaStream_t s) {
+    const W8GroupedPlan pl = plan_w8_grouped(R, E, N, K, gate_up, sm_count_current());
+    CUtensorMap tw, tx;
+    if (!make_w8_grouped_tmap(&tw, q_w, E, N, K, gate_up) ||
+        !make_k128_tmap(&tx, qx, R, K, w8a8_grouped_xbox(pl.bn)))
+        return W4A8_ERR_CUDA;
+    W8GroupedParams p{};
+    p.N = N;
+    p.K = K;
+    p.KB = pl.KB;
+    p.E = E;
+    p.R = R;
+    p.n_tiles = pl.n_tiles;
+    p.offsets = offsets;
+    p.s_w = s_w;
+    p.s_x = s_x;
+    p.Y = Y;
+    p.ldy = ldy;
+    p.vec16 = (aligned16(Y) && ldy % 8 == 0) ? 1 : 0;
+    p.split_tiles = pl.split_tiles;
+    if (pl.split_tiles > 0) {
+        p.partial = static_cast<int32_t*>(workspace);
+        p.counts = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + pl.counts_off);
+        p.epoch = next_epoch();
+    }
+    p.status = dev_status;
+    p.wait_ns = kDefaultWaitNs;
+    return static_cast<w4a8_status>(launch_w8a8_grouped(pl.bn, gate_up, tw, tx, p, pl.grid, s));
+}
+
+w4a8_status check_w8_grouped(int R, int E, const w4a8_wdesc* w) {
+    w4a8_status st = check_w8desc(w);
+    if (st != W4A8_OK) return st;
+    if (R < 0 || E <= 0) return W4A8_ERR_INVALID_ARG;
+    if (E > kGroupedMaxExperts || R > (1 << 24) || w->K > (1 << 17)) return W4A8_ERR_UNSUPPORTED_SHAPE;
+    return W4A8_OK;
+}
+
+// Workspace of the INT8 MoE layer: the W4A8 layer's buffers, then the split
+// partials of the two grouped products (one after the other).
+struct MoeW8Layout {
+    MoeLayout base;
+    size_t split, total;
+};
+
+MoeW8Layout moe_w8_layout(int T, int E, int topk, int H, int I) {
+    MoeW8Layout L{};
+    L.base = moe_layout(T, E, topk, H, I);
+    L.split = L.base.total;
+    const long long R = (long long)T * topk;
+    const int sms = sm_count_current();
+    L.total = L.split + std::max(plan_w8_grouped(R, E, I, H, true, sms).ws_bytes,
+                                 plan_w8_grouped(R, E, H, I, false, sms).ws_bytes);
+    return L;
+}
+
+w4a8_status check_moe_w8(int T, int E, int topk, const w4a8_wdesc* w1, const w4a8_wdesc* w2) {
+    w4a8_status st = check_w8desc(w1);
+    if (st != W4A8_OK) return st;
+    st = check_w8desc(w2);
+    if (st != W4A8_OK) return st;
+    if (T < 0 || E <= 0 || topk <= 0 || topk > E) return W4A8_ERR_INVALID_ARG;
+    const int H = w1->K, I2 = w1->N;
+    if (I2 % 2 != 0 || w2->K != I2 / 2 || w2->N != H) return W4A8_ERR_FORMAT_MISMATCH;
+    if (E > kMaxExperts || topk > 16 || H > 8192 || I2 / 2 > 8192) return W4A8_ERR_UNSUPPORTED_SHAPE;
+    if ((long long)T * topk > (1ll << 24)) return W4A8_ERR_UNSUPPORTED_SHAPE;
+    return W4A8_OK;
 }
 
 // W4A16: (tile, k-block of 64) units; the fp32 partial tiles of a split have
@@ -766,33 +914,13 @@ w4a8_status moe_impl(const uint16_t* X, const float* logits, int T, int E, int t
                                                                     dev_status);
         if ((st = last_cuda()) != W4A8_OK) return st;
     } else {
-        const int epl = (E + 31) / 32;
-        const unsigned blocks = (unsigned)(((long long)T * 32 + 255) / 256);
-        switch (epl) {
-#define W4A8_ROUTE(n) case n: route_topk_kernel<n><<<blocks, 256, 0, s>>>(logits, T, E, topk, topk_idx_out, topk_w_out, dev_status); break;
-            W4A8_ROUTE(1) W4A8_ROUTE(2) W4A8_ROUTE(3) W4A8_ROUTE(4) W4A8_ROUTE(5) W4A8_ROUTE(6) W4A8_ROUTE(7)
-            W4A8_ROUTE(8) W4A8_ROUTE(9) W4A8_ROUTE(10) W4A8_ROUTE(11) W4A8_ROUTE(12) W4A8_ROUTE(13)
-            W4A8_ROUTE(14) W4A8_ROUTE(15) W4A8_ROUTE(16)
-#undef W4A8_ROUTE
-            default: return W4A8_ERR_UNSUPPORTED_SHAPE;
-        }
-        if ((st = last_cuda()) != W4A8_OK) return st;
+        if ((st = launch_route(logits, T, E, topk, topk_idx_out, topk_w_out, dev_status, s)) != W4A8_OK) return st;
     }
     // 2. dispatch
     if (!mark(1)) return W4A8_ERR_CUDA;
-    if (T <= kDispatchThreads) {
-        dispatch_kernel<<<1, kDispatchThreads, 0, s>>>(topk_idx_out, T, E, topk, bn, expert_offsets_out, mtile_off,
-                                                       perm, inv);
-    } else {
-        const int tpc = dispatch_tokens_per_cta(T), C = dispatch_ctas(T);
-        int32_t* dcnt = reinterpret_cast<int32_t*>(ws + L.dcnt);
-        dispatch_count_kernel<<<C, kDispatchThreads, 0, s>>>(topk_idx_out, T, E, topk, tpc, dcnt);
-        if ((st = last_cuda()) != W4A8_OK) return st;
-        dispatch_scan_kernel<<<1, kDispatchScanThreads, 0, s>>>(dcnt, C, E, bn, expert_offsets_out, mtile_off);
-        if ((st = last_cuda()) != W4A8_OK) return st;
-        dispatch_scatter_kernel<<<C, kDispatchThreads, 0, s>>>(topk_idx_out, T, E, topk, tpc, dcnt, perm, inv);
-    }
-    if ((st = last_cuda()) != W4A8_OK) return st;
+    if ((st = launch_dispatch(topk_idx_out, T, E, topk, bn, expert_offsets_out, mtile_off, perm, inv,
+                              reinterpret_cast<int32_t*>(ws + L.dcnt), s)) != W4A8_OK)
+        return st;
     // 3. quantize X straight into dispatch order
     if (!mark(2)) return W4A8_ERR_CUDA;
     if ((st = launch_quant(X, T, H, H, qx, sx, nullptr, 0, inv, topk, dev_status, s)) != W4A8_OK) return st;
@@ -918,18 +1046,7 @@ w4a8_status w4a8_moe_route(const float* logits, int T, int E, int topk, int32_t*
     if (T < 0 || E <= 0 || topk <= 0 || topk > E || E > kMaxExperts || topk > 16) return W4A8_ERR_INVALID_ARG;
     if (T == 0) return W4A8_OK;
     if (!logits || !topk_idx_out || !topk_w_out) return W4A8_ERR_INVALID_ARG;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int epl = (E + 31) / 32;
-    const unsigned blocks = (unsigned)(((long long)T * 32 + 255) / 256);
-    switch (epl) {
-#define W4A8_ROUTE(n) case n: route_topk_kernel<n><<<blocks, 256, 0, s>>>(logits, T, E, topk, topk_idx_out, topk_w_out, dev_status); break;
-        W4A8_ROUTE(1) W4A8_ROUTE(2) W4A8_ROUTE(3) W4A8_ROUTE(4) W4A8_ROUTE(5) W4A8_ROUTE(6) W4A8_ROUTE(7)
-        W4A8_ROUTE(8) W4A8_ROUTE(9) W4A8_ROUTE(10) W4A8_ROUTE(11) W4A8_ROUTE(12) W4A8_ROUTE(13)
-        W4A8_ROUTE(14) W4A8_ROUTE(15) W4A8_ROUTE(16)
-#undef W4A8_ROUTE
-        default: return W4A8_ERR_UNSUPPORTED_SHAPE;
-    }
-    return last_cuda();
+    return launch_route(logits, T, E, topk, topk_idx_out, topk_w_out, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 size_t w4a8_moe_experts_workspace_size(int R, int E, const w4a8_wdesc* w1, const w4a8_wdesc* w2) {
@@ -1043,6 +1160,176 @@ w4a8_status w8a8_linear(const uint16_t* X, int M, int ldx, const int8_t* q_w, co
     st = launch_quant(X, M, w->K, ldx, qx, sx, nullptr, 0, nullptr, 0, dev_status, s);
     if (st != W4A8_OK) return st;
     return w8_gemm_impl(qx, sx, q_w, s_w, w, M, Y, ldy, ws + go, ws_bytes - go, dev_status, stream);
+}
+
+size_t w8a8_grouped_workspace_size(int R, int E, const w4a8_wdesc* w) {
+    if (check_w8_grouped(R, E, w) != W4A8_OK || R == 0) return 0;
+    return plan_w8_grouped(R, E, w->N, w->K, false, sm_count_current()).ws_bytes;
+}
+
+w4a8_status w8a8_grouped_gemm(const int8_t* qx, const float* s_x, const int32_t* offsets, int R, int E,
+                              const int8_t* q_w, const float* s_w, const w4a8_wdesc* w, uint16_t* Y, int ldy,
+                              void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream) {
+    w4a8_status st = check_w8_grouped(R, E, w);
+    if (st != W4A8_OK) return st;
+    if (R == 0) return W4A8_OK;
+    if (!Y || ldy < w->N) return W4A8_ERR_INVALID_ARG;
+    if (!qx || !s_x || !offsets || !q_w || !s_w) return W4A8_ERR_INVALID_ARG;
+    if (!aligned16(qx) || !aligned16(q_w)) return W4A8_ERR_INVALID_ARG;
+    const size_t need = w8a8_grouped_workspace_size(R, E, w);
+    if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return W4A8_ERR_WORKSPACE;
+    return launch_w8_grouped(qx, s_x, offsets, R, E, q_w, s_w, w->N, w->K, false, Y, ldy, workspace, dev_status,
+                             static_cast<cudaStream_t>(stream));
+}
+
+size_t w8a8_grouped_linear_workspace_size(int R, int E, const w4a8_wdesc* w) {
+    if (check_w8_grouped(R, E, w) != W4A8_OK || R == 0) return 0;
+    const size_t sx = align_up((size_t)R * w->K, 256);
+    return align_up(sx + sizeof(float) * (size_t)R, 256) + w8a8_grouped_workspace_size(R, E, w);
+}
+
+w4a8_status w8a8_grouped_linear(const uint16_t* X, int R, int ldx, const int32_t* offsets, int E, const int8_t* q_w,
+                                const float* s_w, const w4a8_wdesc* w, uint16_t* Y, int ldy, void* workspace,
+                                size_t ws_bytes, int32_t* dev_status, void* stream) {
+    w4a8_status st = check_w8_grouped(R, E, w);
+    if (st != W4A8_OK) return st;
+    if (R == 0) return W4A8_OK;
+    if (!Y || ldy < w->N) return W4A8_ERR_INVALID_ARG;
+    if (!X || !offsets || !q_w || !s_w || ldx < w->K || !aligned16(q_w)) return W4A8_ERR_INVALID_ARG;
+    if (ldx % 8 != 0 || !aligned16(X)) return W4A8_ERR_UNSUPPORTED_SHAPE;
+    const size_t need = w8a8_grouped_linear_workspace_size(R, E, w);
+    if (!workspace || ws_bytes < need || !aligned16(workspace)) return W4A8_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const size_t sxo = align_up((size_t)R * w->K, 256);
+    const size_t go = align_up(sxo + sizeof(float) * (size_t)R, 256);
+    int8_t* qx = reinterpret_cast<int8_t*>(ws);
+    float* sx = reinterpret_cast<float*>(ws + sxo);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = launch_quant(X, R, w->K, ldx, qx, sx, nullptr, 0, nullptr, 0, dev_status, s, false,
+                      RowRange{offsets, offsets + E});
+    if (st != W4A8_OK) return st;
+    return launch_w8_grouped(qx, sx, offsets, R, E, q_w, s_w, w->N, w->K, false, Y, ldy, ws + go, dev_status, s);
+}
+
+}  // extern "C"
+
+namespace {
+
+// The INT8 MoE layer; pre_ids (topk = 1): the given expert of every row
+// instead of routing.
+w4a8_status moe_w8_impl(const uint16_t* X, const float* logits, const int32_t* pre_ids, int T, int E, int topk,
+                        const int8_t* w1_q, const float* w1_s, const w4a8_wdesc* w1, const int8_t* w2_q,
+                        const float* w2_s, const w4a8_wdesc* w2, uint16_t* out, int32_t* idx, float* wts,
+                        int32_t* offsets, uint8_t* ws, int32_t* dev_status, cudaStream_t s) {
+    const int H = w1->K, I = w1->N / 2, R = T * topk;
+    const MoeW8Layout L = moe_w8_layout(T, E, topk, H, I);
+    int32_t* inv = reinterpret_cast<int32_t*>(ws + L.base.inv);
+    int8_t* qx = reinterpret_cast<int8_t*>(ws + L.base.qx);
+    float* sx = reinterpret_cast<float*>(ws + L.base.sx);
+    uint16_t* h = reinterpret_cast<uint16_t*>(ws + L.base.h);
+    int8_t* qh = reinterpret_cast<int8_t*>(ws + L.base.qh);
+    float* sh = reinterpret_cast<float*>(ws + L.base.sh);
+    uint16_t* yd = reinterpret_cast<uint16_t*>(ws + L.base.yd);
+    w4a8_status st;
+    if (pre_ids) {
+        preroute_kernel<<<(unsigned)((T + 255) / 256), 256, 0, s>>>(pre_ids, T, E, idx, wts, dev_status);
+        st = last_cuda();
+    } else {
+        st = launch_route(logits, T, E, topk, idx, wts, dev_status, s);
+    }
+    if (st != W4A8_OK) return st;
+    st = launch_dispatch(idx, T, E, topk, 128, offsets, reinterpret_cast<int32_t*>(ws + L.base.mtile_off),
+                         reinterpret_cast<int32_t*>(ws + L.base.perm), inv,
+                         reinterpret_cast<int32_t*>(ws + L.base.dcnt), s);
+    if (st != W4A8_OK) return st;
+    if ((st = launch_quant(X, T, H, H, qx, sx, nullptr, 0, inv, topk, dev_status, s)) != W4A8_OK) return st;
+    st = launch_w8_grouped(qx, sx, offsets, R, E, w1_q, w1_s, I, H, true, h, I, ws + L.split, dev_status, s);
+    if (st != W4A8_OK) return st;
+    if ((st = launch_quant(h, R, I, I, qh, sh, nullptr, 0, nullptr, 0, dev_status, s)) != W4A8_OK) return st;
+    st = launch_w8_grouped(qh, sh, offsets, R, E, w2_q, w2_s, H, I, false, yd, H, ws + L.split, dev_status, s);
+    if (st != W4A8_OK) return st;
+    const long long n = (long long)T * (H / 8);
+    combine_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(yd, wts, inv, T, topk, H, out);
+    return last_cuda();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t w8a8_moe_workspace_size(int T, int E, int topk, const w4a8_wdesc* w1, const w4a8_wdesc* w2) {
+    if (check_moe_w8(T, E, topk, w1, w2) != W4A8_OK || T == 0) return 0;
+    return moe_w8_layout(T, E, topk, w1->K, w1->N / 2).total;
+}
+
+w4a8_status w8a8_moe_grouped_gemm(const uint16_t* X, const float* logits, int T, int E, int topk, const int8_t* w1_q,
+                                  const float* w1_s, const w4a8_wdesc* w1, const int8_t* w2_q, const float* w2_s,
+                                  const w4a8_wdesc* w2, uint16_t* out, int32_t* topk_idx_out, float* topk_w_out,
+                                  int32_t* expert_offsets_out, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                  void* stream) {
+    w4a8_status st = check_moe_w8(T, E, topk, w1, w2);
+    if (st != W4A8_OK) return st;
+    if (T == 0) return W4A8_OK;
+    if (!X || !logits || !w1_q || !w1_s || !w2_q || !w2_s || !out || !topk_idx_out || !topk_w_out ||
+        !expert_offsets_out)
+        return W4A8_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(out) || !aligned16(w1_q) || !aligned16(w2_q)) return W4A8_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < w8a8_moe_workspace_size(T, E, topk, w1, w2) || !aligned16(workspace))
+        return W4A8_ERR_WORKSPACE;
+    return moe_w8_impl(X, logits, nullptr, T, E, topk, w1_q, w1_s, w1, w2_q, w2_s, w2, out, topk_idx_out, topk_w_out,
+                       expert_offsets_out, static_cast<uint8_t*>(workspace), dev_status,
+                       static_cast<cudaStream_t>(stream));
+}
+
+size_t w8a8_moe_experts_workspace_size(int R, int E, const w4a8_wdesc* w1, const w4a8_wdesc* w2) {
+    if (check_moe_w8(R, E, 1, w1, w2) != W4A8_OK || R == 0) return 0;
+    return align_up(moe_w8_layout(R, E, 1, w1->K, w1->N / 2).total, 256) +
+           align_up(sizeof(int32_t) * (2 * (size_t)R + E + 1), 256);
+}
+
+w4a8_status w8a8_moe_experts(const uint16_t* X, const int32_t* expert_ids, int R, int E, const int8_t* w1_q,
+                             const float* w1_s, const w4a8_wdesc* w1, const int8_t* w2_q, const float* w2_s,
+                             const w4a8_wdesc* w2, uint16_t* y_out, void* workspace, size_t ws_bytes,
+                             int32_t* dev_status, void* stream) {
+    w4a8_status st = check_moe_w8(R, E, 1, w1, w2);
+    if (st != W4A8_OK) return st;
+    if (R == 0) return W4A8_OK;
+    if (!X || !expert_ids || !w1_q || !w1_s || !w2_q || !w2_s || !y_out) return W4A8_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(y_out) || !aligned16(w1_q) || !aligned16(w2_q)) return W4A8_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < w8a8_moe_experts_workspace_size(R, E, w1, w2) || !aligned16(workspace))
+        return W4A8_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    // expert ids, weights of one and offsets live past the layer's own workspace
+    int32_t* idx = reinterpret_cast<int32_t*>(ws + align_up(moe_w8_layout(R, E, 1, w1->K, w1->N / 2).total, 256));
+    float* wts = reinterpret_cast<float*>(idx + R);
+    int32_t* offsets = reinterpret_cast<int32_t*>(wts + R);
+    return moe_w8_impl(X, nullptr, expert_ids, R, E, 1, w1_q, w1_s, w1, w2_q, w2_s, w2, y_out, idx, wts, offsets, ws,
+                       dev_status, static_cast<cudaStream_t>(stream));
+}
+
+size_t w4a8_moe_dispatch_workspace_size(int P, int E) {
+    if (P <= 0 || E <= 0 || E > kMaxExperts || P > (1 << 26)) return 0;
+    return align_up(sizeof(int32_t) * (2 * (size_t)P + E + 1 + (size_t)dispatch_ctas(P) * E), 256);
+}
+
+w4a8_status w4a8_moe_dispatch(const int32_t* expert_ids, int P, int E, int32_t* offsets_out, int32_t* perm_out,
+                              int32_t* inv_out, void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream) {
+    if (P < 0 || E <= 0) return W4A8_ERR_INVALID_ARG;
+    if (E > kMaxExperts || P > (1 << 26)) return W4A8_ERR_UNSUPPORTED_SHAPE;
+    if (!offsets_out) return W4A8_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (P == 0)
+        return cudaMemsetAsync(offsets_out, 0, sizeof(int32_t) * (size_t)(E + 1), s) == cudaSuccess ? W4A8_OK
+                                                                                                  : W4A8_ERR_CUDA;
+    if (!expert_ids || !perm_out || !inv_out) return W4A8_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < w4a8_moe_dispatch_workspace_size(P, E)) return W4A8_ERR_WORKSPACE;
+    int32_t* idx = static_cast<int32_t*>(workspace);
+    float* wts = reinterpret_cast<float*>(idx + P);
+    int32_t* mtile_off = reinterpret_cast<int32_t*>(wts + P);
+    preroute_kernel<<<(unsigned)((P + 255) / 256), 256, 0, s>>>(expert_ids, P, E, idx, wts, dev_status);
+    const w4a8_status st = last_cuda();
+    if (st != W4A8_OK) return st;
+    return launch_dispatch(idx, P, E, 1, 128, offsets_out, mtile_off, perm_out, inv_out, mtile_off + E + 1, s);
 }
 
 w4a8_status w4a8_selftest_bounded_wait(int32_t* dev_status, uint64_t limit_ns, void* stream) {

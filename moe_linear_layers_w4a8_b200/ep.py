@@ -3,20 +3,21 @@
 "Kimi 2.7 MoE W4A8 deployment in practice" §5.4 scales the MoE layer by
 spreading the experts over GPUs and exchanging tokens between them.  Here
 rank r of a group of P ranks holds experts [r*E/P, (r+1)*E/P) (packed as for
-w4a8_moe_grouped_gemm) and its own tokens; one forward pass is
+w4a8_moe_grouped_gemm, or as INT8 experts for w8a8_moe_grouped_gemm) and its
+own tokens; one forward pass is
 
   1. route the rank's tokens (w4a8_moe_route);
   2. order the (token, slot) pairs by the rank that owns their expert and
      exchange the activation rows and local expert ids (all-to-all);
-  3. run the received rows through the local experts (w4a8_moe_experts:
-     dispatch, quantization, gate_up + SiLU*up, quantization of h, down);
+  3. run the received rows through the local experts (w4a8_moe_experts or
+     w8a8_moe_experts: dispatch, quantization, gate_up + SiLU*up, quantization of h, down);
   4. send every expert output row back to its token's rank (all-to-all, the
      reverse split);
   5. combine in (token, slot) order (w4a8_moe_combine).
 
 Every row is computed by the same kernels with the same arithmetic as in the
 one-GPU layer, and the combine adds the same values in the same order, so the
-result equals w4a8_moe_grouped_gemm's bit for bit.  The exchanges are plain
+result equals w4a8_moe_grouped_gemm's (w8a8_moe_grouped_gemm's) bit for bit.  The exchanges are plain
 NCCL all-to-alls (bf16 rows travel as raw bit patterns); nothing reads
 another GPU's memory directly.  With one rank (or no process group) the
 exchanges are skipped.
@@ -70,9 +71,12 @@ class ExpertParallelMoE:
             def _route(logits, topk):
                 return m.w4a8_moe_route(logits, topk)
 
+            # INT8 experts (PackedW8) or packed 4-bit ones
+            run = m.w8a8_moe_experts if isinstance(w1_local, m.PackedW8) else m.w4a8_moe_experts
+
             def _experts(rows, ids):
                 x = rows.view(torch.bfloat16)
-                return m.w4a8_moe_experts(x, ids, self.w1, self.w2).view(torch.int16)
+                return run(x, ids, self.w1, self.w2).view(torch.int16)
 
             def _combine(rows, weights):
                 return m.w4a8_moe_combine(rows.view(torch.bfloat16), weights)
