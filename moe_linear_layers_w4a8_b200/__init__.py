@@ -27,7 +27,7 @@ __all__ = [
     "w4a16_gemm", "w4a16_gemm_workspace_size",
     "w8a8_pack_expert_weights", "w8a8_grouped_gemm", "w8a8_grouped_workspace_size", "w8a8_grouped_linear",
     "w8a8_grouped_linear_workspace_size", "w8a8_moe_grouped_gemm", "w8a8_moe_workspace_size", "w8a8_moe_experts",
-    "w4a8_moe_dispatch",
+    "w4a8_moe_dispatch", "w4a16_grouped_gemm",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -168,6 +168,8 @@ def load_library():
         L.w8a8_moe_experts_workspace_size.argtypes = [I, I, D, D]
         L.w8a8_moe_experts.restype = st
         L.w8a8_moe_experts.argtypes = [P, P, I, I, P, P, D, P, P, D, P, P, S, P, P]
+        L.w4a16_grouped_gemm.restype = st
+        L.w4a16_grouped_gemm.argtypes = [P, I, I, P, I, P, P, P, D, P, I, P, P]
         L.w4a8_moe_dispatch_workspace_size.restype = S
         L.w4a8_moe_dispatch_workspace_size.argtypes = [I, I]
         L.w4a8_moe_dispatch.restype = st
@@ -760,6 +762,30 @@ def w8a8_grouped_linear(X: torch.Tensor, offsets: torch.Tensor, w: PackedW8, out
     ws, ws_bytes, _keep = _scratch(workspace, L.w8a8_grouped_linear_workspace_size(R, w.experts, d), dev)
     _launch(dev, "w8a8_grouped_linear", L.w8a8_grouped_linear, X.data_ptr(), R, _row_stride(X), offsets.data_ptr(),
             w.experts, w.q_w.data_ptr(), w.s_w.data_ptr(), d, out.data_ptr(), _row_stride(out), ws, ws_bytes,
+            _addr(status))
+    return out
+
+
+def w4a16_grouped_gemm(X: torch.Tensor, offsets: torch.Tensor, w: PackedWeight, out: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y bf16 [R, N]: rows [offsets[e], offsets[e + 1]) of X bf16 [R, K] (unit
+    column stride) times expert e of the stacked packed weight w, dequantized
+    to bf16 inside the kernel (w4a16_gemm's arithmetic).  Rows that belong to
+    no expert are left as they are in `out`."""
+    L = load_library()
+    where = "w4a16_grouped_gemm"
+    R, _, out = _check_grouped(where, X, offsets, w, out, status)
+    dev, E, d = X.device, w.experts, w.desc
+    _arg(X.dtype == torch.bfloat16 and X.stride(1) == 1, f"{where}: X must be bf16 [R, K] with unit column stride")
+    groups = (E, d.K // d.group, d.N) if d.group > 0 else None
+    _arg(w.packed.dtype == torch.uint8 and w.packed.numel() == E * d.K * d.N // 2 and w.packed.is_contiguous()
+         and w.packed.device == dev, f"{where}: packed must be contiguous uint8 [E, K * N / 2] on {dev}")
+    _arg(w.s_w.dtype == torch.float32 and tuple(w.s_w.shape) == groups and w.s_w.is_contiguous()
+         and w.s_w.device == dev, f"{where}: s_w must be contiguous fp32 [E, G, N] on {dev}")
+    _arg(w.z is None or (w.z.dtype == torch.uint8 and tuple(w.z.shape) == groups and w.z.is_contiguous()
+                         and w.z.device == dev), f"{where}: z must be contiguous uint8 [E, G, N] on {dev}")
+    _launch(dev, where, L.w4a16_grouped_gemm, X.data_ptr(), R, _row_stride(X), offsets.data_ptr(), E,
+            w.packed.data_ptr(), w.s_w.data_ptr(), _addr(w.z), ctypes.byref(d), out.data_ptr(), _row_stride(out),
             _addr(status))
     return out
 

@@ -20,6 +20,7 @@
 #include "gemm_w8a8.cuh"
 #include "gemm_w8a8_grouped.cuh"
 #include "gemm_w4a16.cuh"
+#include "gemm_w4a16_grouped.cuh"
 
 using namespace w4a8;
 
@@ -700,6 +701,47 @@ w4a8_status w16_gemm_impl(const uint16_t* X, int M, int ldx, const uint8_t* pack
                                                  static_cast<cudaStream_t>(stream)));
 }
 
+// The grouped W4A16 product.
+w4a8_status launch_w16_grouped(const uint16_t* X, int ldx, const int32_t* offsets, int R, int E,
+                               const uint8_t* packed, const float* s_w, const uint8_t* z, const w4a8_wdesc* w,
+                               uint16_t* Y, int ldy, int32_t* dev_status, cudaStream_t s) {
+    const int sms = sm_count_current();
+    const long long mean = ((long long)R + E - 1) / E;
+    const int bn = mean > 128 ? 256 : pick_bn(mean);
+    const int G = w->K / w->group;
+    // scale / zero-point rows of one weight stage of 8 k-blocks (stages start at multiples of 8)
+    const int sg_rows = w->group == 64 ? 8 : 4;
+    CUtensorMap tx, ts, tz;
+    if (!make_bf16_k64_tmap(&tx, X, R, w->K, ldx, w4a16_grouped_xrows(bn), w16_box_kb(bn)) ||
+        !make_group_tmap(&ts, s_w, E * G, w->N, true, sg_rows))
+        return W4A8_ERR_CUDA;
+    if (z) {
+        if (!make_group_tmap(&tz, z, E * G, w->N, false, sg_rows)) return W4A8_ERR_CUDA;
+    } else {
+        tz = ts;  // never read by the symmetric kernels
+    }
+    W16GroupedParams p{};
+    p.N = w->N;
+    p.K = w->K;
+    p.KB = w->K / 64;
+    p.E = E;
+    p.R = R;
+    p.G = G;
+    p.group = w->group;
+    p.n_tiles = (w->N + 127) / 128;
+    p.offsets = offsets;
+    p.packed = packed;
+    p.packed_estride = (long long)w->K * w->N / 2;
+    p.sg_rows = sg_rows;
+    p.Y = Y;
+    p.ldy = ldy;
+    p.vec16 = (aligned16(Y) && ldy % 8 == 0) ? 1 : 0;
+    p.status = dev_status;
+    p.wait_ns = kDefaultWaitNs;
+    return static_cast<w4a8_status>(
+        launch_w4a16_grouped(bn, w->symmetric != 0, tx, ts, tz, p, sms <= 0 ? 1 : sms, s));
+}
+
 }  // namespace
 
 // ===================================================================== ABI ==
@@ -1126,6 +1168,24 @@ w4a8_status w4a16_gemm(const uint16_t* X, int M, int ldx, const uint8_t* packed,
                        const w4a8_wdesc* w, uint16_t* Y, int ldy, void* workspace, size_t ws_bytes,
                        int32_t* dev_status, void* stream) {
     return w16_gemm_impl(X, M, ldx, packed, s_w, z, w, Y, ldy, workspace, ws_bytes, dev_status, stream);
+}
+
+w4a8_status w4a16_grouped_gemm(const uint16_t* X, int R, int ldx, const int32_t* offsets, int E,
+                               const uint8_t* packed, const float* s_w, const uint8_t* z, const w4a8_wdesc* w,
+                               uint16_t* Y, int ldy, int32_t* dev_status, void* stream) {
+    w4a8_status st = check_wdesc(w);
+    if (st != W4A8_OK) return st;
+    if (R < 0 || E <= 0) return W4A8_ERR_INVALID_ARG;
+    if (E > kGroupedMaxExperts || R > (1 << 24) || w->K > (1 << 24) ||
+        (long long)E * (w->K / w->group) > (1ll << 30))
+        return W4A8_ERR_UNSUPPORTED_SHAPE;
+    if (R == 0) return W4A8_OK;
+    if (!X || !offsets || !packed || !s_w || !Y || ldx < w->K || ldy < w->N) return W4A8_ERR_INVALID_ARG;
+    if (w->symmetric ? (z != nullptr) : (z == nullptr)) return W4A8_ERR_FORMAT_MISMATCH;
+    if (!aligned16(X) || ldx % 8 != 0 || !aligned16(packed) || !aligned16(s_w) || (z && !aligned16(z)))
+        return W4A8_ERR_INVALID_ARG;
+    return launch_w16_grouped(X, ldx, offsets, R, E, packed, s_w, z, w, Y, ldy, dev_status,
+                              static_cast<cudaStream_t>(stream));
 }
 
 w4a8_status w8a8_gemm(const int8_t* qx, const float* s_x, const int8_t* q_w, const float* s_w, const w4a8_wdesc* w,

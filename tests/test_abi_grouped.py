@@ -119,3 +119,18 @@ def test_binding_refusals():
         m.w8a8_grouped_linear(torch.zeros(2, 128, dtype=torch.bfloat16), off, w)
     with pytest.raises(m.W4A8Error):
         m.w8a8_moe_grouped_gemm(torch.zeros(2, 128, dtype=torch.bfloat16), torch.zeros(2, 4), 2, w, w)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(X=None), 1), (dict(X=ODD), 1), (dict(ldx=500), 1), (dict(ldx=516), 1), (dict(off=None), 1), (dict(ldy=511), 1),
+    (dict(Y=None), 1), (dict(pk=None), 1), (dict(pk=ODD), 1), (dict(sw=None), 1), (dict(sw=ODD), 1),
+    (dict(z=FAKE), 3), (dict(sym=0), 3), (dict(bits=8), 3), (dict(group=32), 3), (dict(N=500), 3),
+    (dict(R=-1), 1), (dict(E=0), 1), (dict(E=513), 2), (dict(R=(1 << 24) + 1), 2), (dict(R=0), 0),
+])
+def test_w4a16_grouped_refusals(lib, kw, code):
+    import moe_linear_layers_w4a8_b200 as m
+    a = dict(X=FAKE, R=16, ldx=512, off=FAKE, E=4, pk=FAKE, sw=FAKE, z=None, Y=FAKE, ldy=512, sym=1, bits=4, group=128, N=512)
+    a.update(kw)
+    d = m.WDesc(a["bits"], a["sym"], a["group"], 512, a["N"], 1)
+    assert lib.w4a16_grouped_gemm(a["X"], a["R"], a["ldx"], a["off"], a["E"], a["pk"], a["sw"], a["z"],
+                                  ctypes.byref(d), a["Y"], a["ldy"], None, None) == code

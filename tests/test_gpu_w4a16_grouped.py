@@ -1,0 +1,238 @@
+"""Grouped W4A16 products (rows sorted by expert, ragged) against the oracle:
+the dequantized weight bit-exact (one-hot rows return it unchanged), outputs
+within 1 bf16 ulp of the correctly rounded exact value, or within the fp32
+accumulation bound where it nearly cancels.
+
+The bound: at most K fp32 additions and, where the sum is split over k, a few
+more, each rounding by 2^-24 of a running magnitude that never exceeds
+sum |x w|; a tensor-core step adds 16 products at once, so K / 16 + 64
+additions, doubled for the sums inside a step."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from synth import gen_linear
+from tests._util import bits, check_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    from moe_linear_layers_w4a8_b200 import _build
+    _build.build()
+    import moe_linear_layers_w4a8_b200 as mm
+    mm.load_library()
+    return mm
+
+
+def fp32_bound(K):
+    return 2.0 * (K / 16 + 64) * 2.0 ** -24
+
+
+def _weights(m, E, K, N, group, sym, seed):
+    g = torch.Generator().manual_seed(seed)
+    W = [torch.randn(K, N, generator=g) * 0.02 + (0.0 if sym else 0.01) for _ in range(E)]
+    w = m.w4a8_pack_expert_weights(lambda e: W[e].cuda(), E, K, N, group, sym, "cuda")
+    return w, W
+
+
+def _dequant(W, group, sym):
+    codes, s, z, bad = O.quant_weights(W.numpy(), group, sym)
+    assert not bad
+    return O.w4a16_dequant(codes, s, None if sym else z, group)
+
+
+def _offsets(counts, front=0):
+    return torch.tensor(np.concatenate([[0], np.cumsum(counts)]) + front, dtype=torch.int32, device="cuda")
+
+
+def _one(w, e, m):
+    return m.PackedWeight(packed=w.packed[e], s_w=w.s_w[e], z=None if w.z is None else w.z[e], desc=w.desc)
+
+
+CASES = [
+    # (counts, K, N, group, symmetric, rows in front, rows behind)
+    ([1], 64, 64, 64, True, 0, 0),
+    ([0, 1, 0], 128, 128, 128, False, 0, 0),
+    ([0, 0], 128, 64, 64, True, 0, 4),
+    ([1] * 6, 2048, 2816, 128, True, 0, 0),                 # a token's six rows
+    ([2, 0, 3, 1], 1344, 1088, 64, False, 0, 2),            # K % 128 == 64
+    ([16, 17, 0, 15, 8, 9, 7], 512, 320, 64, True, 1, 5),   # around small tiles
+    ([33, 1, 64, 65, 2, 0, 31], 448, 576, 64, False, 0, 3),
+    ([64, 63, 65, 1, 128, 129], 640, 192, 128, True, 3, 0),
+    ([256, 257, 5, 255, 300, 511], 384, 128, 128, False, 0, 7),  # 256-row tiles
+    ([700], 256, 64, 64, True, 0, 0),
+    ([3] * 150, 128, 64, 128, True, 0, 0),
+    ([1, 0, 40], 7168, 128, 64, False, 0, 0),               # long k
+    ([24, 0, 1], 4096, 64, 128, True, 0, 0),
+]
+
+
+@pytest.mark.parametrize("counts,K,N,group,sym,front,behind", CASES)
+def test_grouped_gemm(m, counts, K, N, group, sym, front, behind):
+    E, used = len(counts), sum(counts)
+    R = front + used + behind
+    X = gen_linear(R, K, 64, seed=K + N + used).X
+    w, W = _weights(m, E, K, N, group, sym, seed=E * 7 + K)
+    st = m.new_status("cuda")
+    Xc = X.cuda()
+    Xc[:front], Xc[front + used:] = float("nan"), float("inf")   # nobody's rows may hold anything
+    out = torch.full((R, N), -7.0, dtype=torch.bfloat16, device="cuda")
+    Y = m.w4a16_grouped_gemm(Xc, _offsets(counts, front), w, out=out, status=st)
+    assert Y is out and m.w4a8_get_device_status(st) == 0
+    at = front
+    for e, n in enumerate(counts):
+        if n:
+            Ye, A = O.w4a16_gemm(bits(X[at:at + n]), _dequant(W[e], group, sym))
+            check_bf16(bits(Y[at:at + n]), Ye, A, rel=fp32_bound(K), what=f"expert {e}")
+        at += n
+    assert (out[:front] == -7).all() and (out[front + used:] == -7).all()
+    # the same bits in every run
+    again = m.w4a16_grouped_gemm(Xc, _offsets(counts, front), w, out=torch.full_like(out, -7.0))
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("K,N,group,sym", [
+    (256, 192, 128, True), (256, 192, 128, False), (320, 128, 64, True), (320, 128, 64, False),
+])
+@pytest.mark.parametrize("rows", [5, 16, 40, 256])
+def test_dequantized_weight_is_exact(m, K, N, group, sym, rows):
+    """One-hot rows (`rows` of them for each expert) return weight rows unchanged."""
+    E = 2 * ((K + rows - 1) // rows)
+    w, W = _weights(m, 2, K, N, group, sym, seed=K + rows)
+    pick = torch.arange(E) % 2       # experts alternate between the two weights
+    big = m.PackedWeight(packed=w.packed[pick].contiguous(), s_w=w.s_w[pick].contiguous(),
+                         z=None if sym else w.z[pick].contiguous(), desc=w.desc, experts=E)
+    eye = torch.eye(K, dtype=torch.bfloat16, device="cuda")
+    parts = [eye[(e // 2) * rows:(e // 2 + 1) * rows] for e in range(E)]
+    Y = m.w4a16_grouped_gemm(torch.cat(parts), _offsets([len(p) for p in parts]), big)
+    Wh = [_dequant(x, group, sym) for x in W]
+    at = 0
+    for e, part in enumerate(parts):
+        assert np.array_equal(bits(Y[at:at + len(part)]), Wh[e % 2][(e // 2) * rows:(e // 2) * rows + len(part)])
+        at += len(part)
+
+
+def test_layer_size_sampled_experts(m):
+    g = torch.Generator().manual_seed(3)
+    counts = torch.bincount(torch.randint(0, 64, (12288,), generator=g), minlength=64).tolist()
+    w, W = _weights(m, 64, 1408, 2048, 128, True, seed=1)
+    X = gen_linear(12288, 1408, 64, seed=4).X
+    Y = m.w4a16_grouped_gemm(X.cuda(), _offsets(counts), w)
+    at = 0
+    for e, n in enumerate(counts):
+        if e in (0, 63):
+            Ye, A = O.w4a16_gemm(bits(X[at:at + n]), _dequant(W[e], 128, True))
+            check_bf16(bits(Y[at:at + n]), Ye, A, rel=fp32_bound(1408), what=f"expert {e}")
+        at += n
+
+
+def test_strided_rows_and_outputs(m):
+    for counts in ([20, 0, 29, 1], [2, 1, 0, 2]):
+        R = sum(counts)
+        w, _ = _weights(m, 4, 384, 128, 64, False, seed=5)
+        wide = torch.randn(R, 400, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+        X, off = wide[:, :384], _offsets(counts)
+        want = m.w4a16_grouped_gemm(X.contiguous(), off, w)
+        for pitch in (128, 136, 131):
+            buf = torch.full((R, pitch), 9.0, dtype=torch.bfloat16, device="cuda")
+            m.w4a16_grouped_gemm(X, off, w, out=buf[:, :128])
+            assert torch.equal(buf[:, :128], want) and (buf[:, 128:] == 9).all()
+
+
+@pytest.mark.parametrize("off", [[0, 5, 3, 12], [-1, 2, 4, 12], [0, 4, 8, 13], [12, 0, 12, 5], [0, 2**31 - 1, 5, 6]])
+def test_bad_offsets_are_reported(m, off):
+    w, _ = _weights(m, 3, 128, 64, 64, True, seed=6)
+    st = m.new_status("cuda")
+    guard = torch.full((14, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    m.w4a16_grouped_gemm(torch.randn(12, 128).bfloat16().cuda(), torch.tensor(off, dtype=torch.int32, device="cuda"),
+                         w, out=guard[1:13], status=st)
+    assert m.w4a8_get_device_status(st) == 1
+    assert (guard[0] == 5).all() and (guard[13] == 5).all()
+
+
+def test_nonfinite_rows_stay_in_their_row(m):
+    """A NaN or infinite activation reaches its own row of the output alone."""
+    for counts in ([3, 2], [40, 30]):
+        R = sum(counts)
+        w, _ = _weights(m, 2, 256, 128, 128, True, seed=7)
+        X = torch.randn(R, 256, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+        off = _offsets(counts)
+        want = m.w4a16_grouped_gemm(X, off, w)
+        X[1, 7], X[R - 2, 100] = float("nan"), float("inf")
+        got = m.w4a16_grouped_gemm(X, off, w)
+        keep = [r for r in range(R) if r not in (1, R - 2)]
+        assert torch.equal(got[keep], want[keep])
+        assert torch.isnan(got[1]).all() and not torch.isfinite(got[R - 2]).any()
+
+
+def test_captured_with_changing_offsets(m):
+    w, _ = _weights(m, 4, 512, 256, 128, True, seed=8)
+    X = torch.randn(48, 512, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    off, out = _offsets([12, 12, 12, 12]), torch.zeros(48, 256, dtype=torch.bfloat16, device="cuda")
+    m.w4a16_grouped_gemm(X, off, w, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.w4a16_grouped_gemm(X, off, w, out=out)
+    for counts in ([12, 12, 12, 12], [0, 48, 0, 0], [1, 0, 0, 2]):
+        off.copy_(_offsets(counts))
+        want = m.w4a16_grouped_gemm(X, off, w, out=torch.zeros_like(out))
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+
+
+def test_experts_of_a_layer(m):
+    """Route, dispatch, gather, gate_up, silu * up, down, combine with the
+    packed weights a W4A8 layer uses; against the same steps in fp64 on the
+    dequantized weights (bf16 roundings of gate_up, h and the expert rows:
+    2^-9 of each value and a few times that in the sums)."""
+    T, E, topk, H, I, group = 40, 6, 2, 512, 256, 128
+    w1, W1 = _weights(m, E, H, 2 * I, group, True, seed=1)
+    w2, W2 = _weights(m, E, I, H, group, True, seed=2)
+    g = torch.Generator().manual_seed(5)
+    X = torch.randn(T, H, generator=g).bfloat16().cuda()
+    logits = torch.randn(T, E, generator=g).cuda()
+    idx, wt = m.w4a8_moe_route(logits, topk)
+    offsets, perm, inv = m.w4a8_moe_dispatch(idx, E)
+    rows = X[torch.div(perm, topk, rounding_mode="floor").long()]
+    gu = m.w4a16_grouped_gemm(rows, offsets, w1).float()
+    h = (torch.nn.functional.silu(gu[:, :I]) * gu[:, I:]).bfloat16()
+    out = m.w4a8_moe_combine(m.w4a16_grouped_gemm(h, offsets, w2)[inv.long()], wt)
+    f64 = lambda W: torch.from_numpy(O.bf16_to_f32(_dequant(W, group, True)).astype(np.float64))  # noqa: E731
+    ref = torch.zeros(T, H, dtype=torch.float64)
+    for t in range(T):
+        for j in range(topk):
+            e = int(idx[t, j])
+            y = X[t].double().cpu() @ f64(W1[e])
+            y = (y[:I] / (1 + torch.exp(-y[:I])) * y[I:]) @ f64(W2[e])
+            ref[t] += float(wt[t, j]) * y
+    err = (out.double().cpu() - ref).norm() / ref.norm()
+    assert err <= 4 * 2.0 ** -8
+
+
+def test_refusals_of_the_binding(m):
+    w, _ = _weights(m, 4, 256, 64, 64, False, seed=11)
+    X, off = torch.randn(8, 256).bfloat16().cuda(), _offsets([2, 2, 2, 2])
+
+    def refused(code, *a, **k):
+        with pytest.raises(m.W4A8Error) as e:
+            m.w4a16_grouped_gemm(*a, **k)
+        assert e.value.code == code
+
+    refused(1, X.float(), off, w)
+    refused(1, X.t().contiguous().t(), off, w)
+    refused(1, X[:, 1:], off, w)
+    refused(1, X, off.long(), w)
+    refused(1, X, off[:4], w)
+    refused(1, X, off, _one(w, 0, m))
+    refused(1, X, off, w, out=torch.empty(8, 64, device="cuda"))
+    refused(3, X, off, m.PackedWeight(w.packed, w.s_w, None, w.desc, 4))
+    refused(1, X, off, m.PackedWeight(w.packed, w.s_w[:, :1], w.z, w.desc, 4))
+    refused(1, X, off, m.PackedWeight(w.packed[:2], w.s_w, w.z, w.desc, 4))
+    odd = torch.randn(8, 260).bfloat16().cuda()[:, :256]      # pitch not a multiple of 16 bytes
+    refused(1, odd, off, w)
+    assert m.w4a16_grouped_gemm(X[:0], torch.zeros_like(off), w).shape == (0, 64)
