@@ -399,25 +399,28 @@ W4A8_API w4a8_status w4a16_gemm(const uint16_t* X, int M, int ldx, const uint8_t
                                 const uint8_t* z, const w4a8_wdesc* w, uint16_t* Y, int ldy, void* workspace,
                                 size_t ws_bytes, int32_t* dev_status, void* stream);
 
+/* Workspace bytes w4a16_grouped_gemm needs for R rows (0 when none). */
+W4A8_API size_t w4a16_grouped_workspace_size(int R, int E, const w4a8_wdesc* w);
+
 /* w4a16_grouped_gemm — the rows of an MoE layer, sorted by expert, times their
  * expert's packed 4-bit weight: w4a16_gemm's arithmetic on every row, with
  * offsets as for w8a8_grouped_gemm (rows that belong to nobody are neither
- * used nor written).  fp32 sums are taken in an order that depends on the
- * launch's tile, so a row's result may differ by an fp32 rounding from
+ * used nor written).  Few tiles are split along k and their fp32 partial tiles
+ * added in the order of k, so a row's result may differ by fp32 roundings from
  * w4a16_gemm's; it is the same in every run of the same call.
  * X        device bf16 [R][ldx], 16-byte aligned, ldx % 8 == 0, ldx >= K.
  * packed, s_w, z: E stacked w4a8_pack_weights results (packed
  *          w4a8_packed_bytes(K, N) bytes each, s_w fp32 [E][G][N], z uint8
  *          [E][G][N], NULL iff symmetric), 16-byte aligned; w describes one.
  * Y        device bf16 [R][ldy], ldy >= N.
- * Needs no workspace.
- * Limits: E <= 512, R <= 2^24, K <= 2^24.
- * Errors: INVALID_ARG, FORMAT_MISMATCH, UNSUPPORTED_SHAPE, CUDA; INVALID_ARG
- *         (offsets) and TIMEOUT via dev_status. */
+ * workspace, ws_bytes: as for w8a8_grouped_gemm.
+ * Limits: E <= 512, R <= 2^24, K <= 2^17.
+ * Errors: INVALID_ARG, FORMAT_MISMATCH, UNSUPPORTED_SHAPE, WORKSPACE, CUDA;
+ *         INVALID_ARG (offsets) and TIMEOUT via dev_status. */
 W4A8_API w4a8_status w4a16_grouped_gemm(const uint16_t* X, int R, int ldx, const int32_t* offsets, int E,
                                         const uint8_t* packed, const float* s_w, const uint8_t* z,
-                                        const w4a8_wdesc* w, uint16_t* Y, int ldy, int32_t* dev_status,
-                                        void* stream);
+                                        const w4a8_wdesc* w, uint16_t* Y, int ldy, void* workspace, size_t ws_bytes,
+                                        int32_t* dev_status, void* stream);
 
 /*
  * w4a8_moe_grouped_gemm — one MoE expert layer, following "Kimi 2.7 MoE,

@@ -27,7 +27,7 @@ __all__ = [
     "w4a16_gemm", "w4a16_gemm_workspace_size",
     "w8a8_pack_expert_weights", "w8a8_grouped_gemm", "w8a8_grouped_workspace_size", "w8a8_grouped_linear",
     "w8a8_grouped_linear_workspace_size", "w8a8_moe_grouped_gemm", "w8a8_moe_workspace_size", "w8a8_moe_experts",
-    "w4a8_moe_dispatch", "w4a16_grouped_gemm",
+    "w4a8_moe_dispatch", "w4a16_grouped_gemm", "w4a16_grouped_workspace_size",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -169,7 +169,9 @@ def load_library():
         L.w8a8_moe_experts.restype = st
         L.w8a8_moe_experts.argtypes = [P, P, I, I, P, P, D, P, P, D, P, P, S, P, P]
         L.w4a16_grouped_gemm.restype = st
-        L.w4a16_grouped_gemm.argtypes = [P, I, I, P, I, P, P, P, D, P, I, P, P]
+        L.w4a16_grouped_gemm.argtypes = [P, I, I, P, I, P, P, P, D, P, I, P, S, P, P]
+        L.w4a16_grouped_workspace_size.restype = S
+        L.w4a16_grouped_workspace_size.argtypes = [I, I, D]
         L.w4a8_moe_dispatch_workspace_size.restype = S
         L.w4a8_moe_dispatch_workspace_size.argtypes = [I, I]
         L.w4a8_moe_dispatch.restype = st
@@ -766,7 +768,12 @@ def w8a8_grouped_linear(X: torch.Tensor, offsets: torch.Tensor, w: PackedW8, out
     return out
 
 
+def w4a16_grouped_workspace_size(R: int, w: PackedWeight) -> int:
+    return int(load_library().w4a16_grouped_workspace_size(int(R), w.experts, ctypes.byref(w.desc)))
+
+
 def w4a16_grouped_gemm(X: torch.Tensor, offsets: torch.Tensor, w: PackedWeight, out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None,
                        status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y bf16 [R, N]: rows [offsets[e], offsets[e + 1]) of X bf16 [R, K] (unit
     column stride) times expert e of the stacked packed weight w, dequantized
@@ -784,9 +791,10 @@ def w4a16_grouped_gemm(X: torch.Tensor, offsets: torch.Tensor, w: PackedWeight, 
          and w.s_w.device == dev, f"{where}: s_w must be contiguous fp32 [E, G, N] on {dev}")
     _arg(w.z is None or (w.z.dtype == torch.uint8 and tuple(w.z.shape) == groups and w.z.is_contiguous()
                          and w.z.device == dev), f"{where}: z must be contiguous uint8 [E, G, N] on {dev}")
+    ws, ws_bytes, _keep = _scratch(workspace, L.w4a16_grouped_workspace_size(R, E, ctypes.byref(d)), dev)
     _launch(dev, where, L.w4a16_grouped_gemm, X.data_ptr(), R, _row_stride(X), offsets.data_ptr(), E,
-            w.packed.data_ptr(), w.s_w.data_ptr(), _addr(w.z), ctypes.byref(d), out.data_ptr(), _row_stride(out),
-            _addr(status))
+            w.packed.data_ptr(), w.s_w.data_ptr(), _addr(w.z), ctypes.byref(d), out.data_ptr(), _row_stride(out), ws,
+            ws_bytes, _addr(status))
     return out
 
 

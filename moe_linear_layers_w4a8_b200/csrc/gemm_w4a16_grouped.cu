@@ -7,8 +7,8 @@
 namespace w4a8 {
 
 template <int BN, bool SYM>
-static int launch_w4a16_grouped_t(const CUtensorMap& tmap_x, const CUtensorMap& tmap_s, const CUtensorMap& tmap_z,
-                                  const W16GroupedParams& p, int grid, cudaStream_t stream) {
+static int launch_w4a16_grouped_t(const CUtensorMap& tmap_x, const CUtensorMap& tmap_xs, const CUtensorMap& tmap_s,
+                                  const CUtensorMap& tmap_z, const W16GroupedParams& p, int grid, cudaStream_t stream) {
     using C = W16GCfg<BN>;
     auto kern = w4a16_grouped_kernel<BN, SYM>;
     static std::atomic<uint64_t> attr_done{0};
@@ -22,7 +22,7 @@ static int launch_w4a16_grouped_t(const CUtensorMap& tmap_x, const CUtensorMap& 
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kW16Threads);
+    cfg.blockDim = dim3(kW16GThreads);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -30,18 +30,18 @@ static int launch_w4a16_grouped_t(const CUtensorMap& tmap_x, const CUtensorMap& 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, tmap_x, tmap_s, tmap_z, p) != cudaSuccess) return 6;
+    if (cudaLaunchKernelEx(&cfg, kern, tmap_x, tmap_xs, tmap_s, tmap_z, p) != cudaSuccess) return 6;
     return cudaGetLastError() == cudaSuccess ? 0 : 6;
 }
 
-int launch_w4a16_grouped(int bn, bool sym, const CUtensorMap& tx, const CUtensorMap& ts, const CUtensorMap& tz,
-                         const W16GroupedParams& p, int grid, cudaStream_t stream) {
+int launch_w4a16_grouped(int bn, bool sym, const CUtensorMap& tx, const CUtensorMap& txs, const CUtensorMap& ts,
+                         const CUtensorMap& tz, const W16GroupedParams& p, int grid, cudaStream_t stream) {
 #define W4A8_W16G(B)                                                                   \
     case B:                                                                            \
-        return sym ? launch_w4a16_grouped_t<B, true>(tx, ts, tz, p, grid, stream)      \
-                   : launch_w4a16_grouped_t<B, false>(tx, ts, tz, p, grid, stream);
+        return sym ? launch_w4a16_grouped_t<B, true>(tx, txs, ts, tz, p, grid, stream)      \
+                   : launch_w4a16_grouped_t<B, false>(tx, txs, ts, tz, p, grid, stream);
     switch (bn) {
-        W4A8_W16G(16) W4A8_W16G(32) W4A8_W16G(64) W4A8_W16G(128) W4A8_W16G(256)
+        W4A8_W16G(16) W4A8_W16G(32) W4A8_W16G(64) W4A8_W16G(128) W4A8_W16G(224)
     }
 #undef W4A8_W16G
     return 2;

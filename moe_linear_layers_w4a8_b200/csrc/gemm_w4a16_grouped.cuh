@@ -5,16 +5,36 @@
 //   w_hat[e,k,n] = bf16( fp32( s_w[e,g,n] * (q[e,k,n] - z[e,g,n]) ) )  g = k / group
 //   y[r,n]       = bf16( sum_k x[r,k] * w_hat[e,k,n] )   e = expert of row r, fp32 sums
 //
-// The tile kernel (many rows for each expert).  The pipeline of the dense
-// W4A16 kernel (gemm_w4a16.cuh: weight ring, activation ring, eight warps that
-// dequantize into a swizzled A ring, one MMA thread, two accumulators in TMEM)
-// over the tile list of the grouped W8A8 kernel (gemm_w8a8_grouped.cuh): every
-// CTA derives tiles from the device offsets, hands them out round-robin, sets
-// the MMA's N to the tile's rows and loads no more activation boxes than they
-// need.
+// Design (B200): the tiles of the grouped W8A8 kernel (gemm_w8a8_grouped.cuh:
+// every CTA derives them from the device offsets; whole tiles round-robin, or
+// equal ranges of k with partial tiles added by the CTA that comes last) around
+// the dequantization of the dense W4A16 kernel (gemm_w4a16.cuh).
+//   * Swap-AB: 128 weight columns are the MMA's rows, up to BN tokens its
+//     columns; its N is set to the tile's rows, and few rows take small
+//     activation boxes.
+//   * A stage is two k-blocks of 64: the dequantized bf16 weights (A) and the
+//     rows (B), both in the MMA's 128-byte swizzled layout.  One lane issues the
+//     eight MMAs of a stage between one wait and one commit: per k-block that
+//     costs it 250 cycles, with a wait and a commit for each half of that 600.
+//   * 16 warps dequantize, four teams of 4, k-blocks in turn, so that one team's
+//     waits, stores and proxy fence (500 of its 2400 cycles) overlap the others'
+//     arithmetic.  A thread takes one column's 64 k of a k-block: one scale,
+//     two 16-byte code chunks, eight 16-byte stores.  It gives the stage of
+//     packed weights back as soon as the codes are in its registers.
+//   * Bound by the dequantization: about 22 instructions for 8 weights, 13 of
+//     them integer ones at half rate (a mask as an immediate and 2^23 in a
+//     register: with a second constant for the flipped bit each mask cost one
+//     move more, 424 -> 369 us), plus 8 for the stores and hand-over.  Measured
+//     0.33 us per k-block of 64 and CTA at any number of rows, which is the time
+//     of the MMAs at 170 rows.
+// Tried and taken out: a kernel on mma.sync whose lanes keep the weights they
+// dequantize (no shared memory between the two); its instructions for the
+// fragments outweighed the hand-over: 280 us against 259 (512 rows, 32 experts,
+// K = 7168, N = 4096, groups of 64).
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -25,47 +45,121 @@ namespace w4a8 {
 
 struct W16GroupedParams {
     int N, K, KB;                // KB = K / 64 k-blocks
+    int units;                   // stages of two k-blocks of a tile
     int E, R, G, group;
     int n_tiles;                 // ceil(N / 128)
     const int32_t* offsets;      // [E + 1] device
     const uint8_t* packed;       // E stacked packed weights
     long long packed_estride;    // bytes between experts
-    int sg_rows;                 // rows (groups) of the scale / zero-point boxes
     uint16_t* Y;
     int ldy;
     int vec16;
+    int split_tiles;             // tiles below which units may be split (0: never)
+    float* partial;              // [2 * grid][BN][128] fp32 partial tiles
+    unsigned long long* counts;  // [split_tiles] arrivals of this launch
+    unsigned long long epoch;
     int32_t* status;
     unsigned long long wait_ns;
 };
 
+constexpr int kW16GThreads = 736;      // weight producer, MMA, 4 epilogue warps, 16 dequant warps, row producer
+constexpr int kW16GEpiWarp0 = 2;
+constexpr int kW16GDqWarp0 = 6;
+constexpr int kW16GDqWarps = 16;       // four teams of 4, k-blocks in turn; two teams fill a stage
+constexpr int kW16GTeams = 4;
+constexpr int kW16GXWarp = 22;
+constexpr int kW16GKSW = 2;            // k-blocks of 64 per stage of packed weights: those of one pair of teams
+constexpr int kW16GSmall = 32;         // rows of the small activation box
+
+// Rows of the large activation box (one k-block) of a tile of bn rows.
+__host__ __device__ constexpr int w4a16_grouped_xrows(int bn) { return bn == 224 ? 112 : bn; }
+
 template <int BN>
-struct W16GCfg : W16Cfg<BN> {
-    using B = W16Cfg<BN>;
-    static constexpr int XROWS = BN < 128 ? BN : 128;       // rows per activation request
-    static constexpr int STG = 4 * 2048;                    // output staging: 32 tokens x 32 columns per warp
-    static constexpr int OFF_BAR = B::OFF_Y + STG;
-    static constexpr int OFF_TABLE = OFF_BAR + B::NUM_BARS * 8;
+struct W16GCfg {
+    static constexpr int XB = BN * 128;                    // one k-block of activations: BN rows x 64 k bf16
+    static constexpr int A_BYTES = 128 * 128;              // one k-block of bf16 weights: 128 columns x 64 k
+    static constexpr int STAGE = 2 * (A_BYTES + XB);       // two k-blocks: weights, then activations
+    static constexpr int NS = BN <= 32 ? 4 : 2;            // stages: unit % NS of every tile
+    static constexpr int XROWS = w4a16_grouped_xrows(BN);  // rows of the large activation box
+    static constexpr int KSW = kW16GKSW;
+    static constexpr int PK_HALF = KSW * 2048;             // codes of one 64-column half
+    static constexpr int W_S = 2 * PK_HALF;                // fp32 scales [KSW][128]
+    static constexpr int W_Z = W_S + KSW * 512;            // zero-points [KSW][128]
+    static constexpr int W_STAGE = W_Z + KSW * 128;
+    static constexpr int NW = 4;                                     // stages of packed weights: unit % NW of every tile
+    static constexpr int STG = BN == 224 ? 4 * 1024 : 4 * 2048;   // output staging: LB tokens x 32 columns per warp
+    static constexpr int OFF_W = NS * STAGE;
+    static constexpr int OFF_Y = OFF_W + NW * W_STAGE;
+    static constexpr int OFF_BAR = OFF_Y + STG;
+    static constexpr int NUM_BARS = 2 * NW + 2 * NS + 5;
+    static constexpr int OFF_TABLE = OFF_BAR + NUM_BARS * 8;
     static constexpr int TABLE = 3 * (kGroupedMaxExperts + 1) * 4;
     static constexpr int OFF_MISC = OFF_TABLE + TABLE;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static constexpr uint32_t TMEM_COLS = BN == 224 ? 512 : 2 * BN;
+    static constexpr int SPLIT_GAIN = 3 + BN / 64;         // stages of 128 k (a partial tile is BN / 2 KB)
+    static constexpr int LB = BN == 224 || BN < 32 ? 16 : 32;   // tokens per epilogue batch
+    static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128 || BN == 224, "BN");
+    static_assert(W_S % 128 == 0 && W_STAGE % 128 == 0, "TMA destinations");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
+// Scale and zero-point of a column's group for dequant_word32: pairs for the
+// nibbles of the first and of the second byte of a halfword (a = -(2^23 + z
+// 16^p): a paired subtraction would negate its operand first).
+template <bool SYM>
+struct NibblePairs {
+    uint64_t s01, s23, a01, a23;
+    __device__ __forceinline__ void set(float s, uint32_t z) {
+        s01 = f2_from_bits(__float_as_uint(s), __float_as_uint(s * 0x1p-4f));
+        s23 = f2_from_bits(__float_as_uint(s * 0x1p-8f), __float_as_uint(s * 0x1p-12f));
+        const uint32_t zc = SYM ? 8u : z;
+        a01 = f2_from_bits(0xCB000000u | zc, 0xCB000000u | (zc << 4));
+        a23 = f2_from_bits(0xCB000000u | (zc << 8), 0xCB000000u | (zc << 12));
+    }
+};
+
+// The bits of w under mask in the mantissa of 2^23.  The mask is an immediate
+// and 2^23 a register; a second constant would cost a move each time.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t magic_bits(uint32_t w) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "n"(MASK), "r"(0x4B000000u));  // (w & mask) | 2^23
+    return d;
+}
+
+// dequant_chunk's arithmetic for one word (bytes 0-3): lo / hi = its low and
+// high nibbles' weights, two bf16 pairs each in byte order.  Symmetric codes
+// are two's complement; with bit 3 flipped they are q + 8.
+template <bool SYM>
+__device__ __forceinline__ void dequant_word32(uint32_t w, const NibblePairs<SYM>& q, uint32_t* lo, uint32_t* hi) {
+    if (SYM) w ^= 0x88888888u;
+    const uint32_t v = w >> 16;
+    float l0, l1, l2, l3, h0, h1, h2, h3;
+    f2_split(f2_mul(f2_add(f2_from_bits(magic_bits<0xFu>(w), magic_bits<0xF0u>(w)), q.a01), q.s01), l0, h0);
+    f2_split(f2_mul(f2_add(f2_from_bits(magic_bits<0xF00u>(w), magic_bits<0xF000u>(w)), q.a23), q.s23), l1, h1);
+    f2_split(f2_mul(f2_add(f2_from_bits(magic_bits<0xFu>(v), magic_bits<0xF0u>(v)), q.a01), q.s01), l2, h2);
+    f2_split(f2_mul(f2_add(f2_from_bits(magic_bits<0xF00u>(v), magic_bits<0xF000u>(v)), q.a23), q.s23), l3, h3);
+    lo[0] = pack_bf16x2(l0, l1);
+    lo[1] = pack_bf16x2(l2, l3);
+    hi[0] = pack_bf16x2(h0, h1);
+    hi[1] = pack_bf16x2(h2, h3);
+}
+
 template <int BN, bool SYM>
-__global__ void __launch_bounds__(kW16Threads, 1)
-    w4a16_grouped_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_s,
-                         const __grid_constant__ CUtensorMap tmap_z, const W16GroupedParams p) {
+__global__ void __launch_bounds__(kW16GThreads, 1)
+    w4a16_grouped_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_xs,
+                         const __grid_constant__ CUtensorMap tmap_s, const __grid_constant__ CUtensorMap tmap_z,
+                         const W16GroupedParams p) {
     using C = W16GCfg<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* w_full = bars;                   // [NW] codes, scales, zero-points landed
-    uint64_t* w_empty = w_full + C::NW;        // [NW] the 8 dequant warps read them
-    uint64_t* x_full = w_empty + C::NW;        // [NX] activation boxes landed
-    uint64_t* x_empty = x_full + C::NX;        // [NX] their MMAs completed
-    uint64_t* a_full = x_empty + C::NX;        // [NA] bf16 weight tile written
-    uint64_t* a_empty = a_full + C::NA;        // [NA] its MMAs completed
-    uint64_t* acc_full = a_empty + C::NA;      // [2]
+    uint64_t* w_empty = w_full + C::NW;        // [NW] the 16 dequant warps read them
+    uint64_t* full = w_empty + C::NW;          // [NS] weights written by a team, activations landed
+    uint64_t* empty = full + C::NS;            // [NS] their MMAs completed
+    uint64_t* acc_full = empty + C::NS;        // [2]
     uint64_t* acc_empty = acc_full + 2;        // [2]
     uint64_t* drain = acc_empty + 2;           // [1]
     GroupTable g;
@@ -74,6 +168,7 @@ __global__ void __launch_bounds__(kW16Threads, 1)
     g.mt = g.cnt + kGroupedMaxExperts + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 4);
+    int* last_flag = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -81,15 +176,11 @@ __global__ void __launch_bounds__(kW16Threads, 1)
         pdl_launch_dependents();
         for (int i = 0; i < C::NW; ++i) {
             mbar_init(&w_full[i], 1);
-            mbar_init(&w_empty[i], kW16DqWarps);
+            mbar_init(&w_empty[i], kW16GDqWarps / 2);
         }
-        for (int i = 0; i < C::NX; ++i) {
-            mbar_init(&x_full[i], 1);
-            mbar_init(&x_empty[i], 1);
-        }
-        for (int i = 0; i < C::NA; ++i) {
-            mbar_init(&a_full[i], kW16DqWarps);
-            mbar_init(&a_empty[i], 1);
+        for (int i = 0; i < C::NS; ++i) {
+            mbar_init(&full[i], kW16GDqWarps / 2 + 1);
+            mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -115,236 +206,274 @@ __global__ void __launch_bounds__(kW16Threads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const WaitCtx wc{abort_flag, p.status, wait_cycles_for_ns(p.wait_ns)};
-    GroupedWalk walk(g, p.E, p.n_tiles, p.KB, 0);
+    GroupedWalk walk(g, p.E, p.n_tiles, p.units, p.split_tiles, C::SPLIT_GAIN);
     const int KB = p.KB;
     const int kb_shift = p.group == 128 ? 1 : 0;   // k-blocks of 64 per group: 1 << kb_shift
     long long tile;
-    int kb_first, kb_end;                           // always 0 and KB: whole tiles
+    int u0, u1;                                     // the segment's stages
 
     if (warp == 0) {
         // ------------------------------------------ producer: weight ring --
         if (lane == 0) {
-            Ring rw;
-            long long issued = 0;
+            uint32_t phases = 0u;    // parity of every stage's next fill
+            uint32_t used = 0u;      // stages that have been filled
             bool ok = true;
-            while (ok && walk.next(tile, kb_first, kb_end)) {
+            const int sg_rows = C::KSW >> kb_shift;
+            while (ok && walk.next(tile, u0, u1)) {
                 const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
                 const int halves = min(128, p.N - gt.nt * 128) / 64;
                 const uint8_t* codes = p.packed + gt.e * p.packed_estride;
-                for (int kb = 0; kb < KB; kb += kW16KSW) {
-                    const int len = min(kW16KSW, KB - kb);
-                    if (!wait_bounded(&w_empty[rw.idx], rw.phase ^ 1u, wc)) { ok = false; break; }
-                    uint32_t bytes = halves * len * 2048 + p.sg_rows * 512;
-                    if (!SYM) bytes += p.sg_rows * 128;
-                    mbar_arrive_expect_tx(&w_full[rw.idx], bytes);
-                    uint8_t* st = smem + C::OFF_W + rw.idx * C::W_STAGE;
+                for (int u = u0; u < u1; ++u) {
+                    const int kb = 2 * u, len = min(C::KSW, KB - kb);
+                    const int slot = u & (C::NW - 1);
+                    if (!wait_bounded(&w_empty[slot], ((phases >> slot) & 1u) ^ 1u, wc)) { ok = false; break; }
+                    uint32_t bytes = halves * len * 2048 + sg_rows * 512;
+                    if (!SYM) bytes += sg_rows * 128;
+                    mbar_arrive_expect_tx(&w_full[slot], bytes);
+                    uint8_t* st = smem + C::OFF_W + slot * C::W_STAGE;
                     // 64 columns x 32 k are 1 KB; a column block's chunks follow one another over all of K
                     for (int hf = 0; hf < halves; ++hf)
                         bulk_load(st + hf * C::PK_HALF, codes + ((long long)(gt.nt * 2 + hf) * KB + kb) * 2048,
-                                  len * 2048, &w_full[rw.idx]);
+                                  len * 2048, &w_full[slot]);
                     const int g0 = gt.e * p.G + (kb >> kb_shift);
-                    tma_load_2d(st + C::W_S, &tmap_s, &w_full[rw.idx], gt.nt * 128, g0);
-                    if (!SYM) tma_load_2d(st + C::W_Z, &tmap_z, &w_full[rw.idx], gt.nt * 128, g0);
-                    rw.next(C::NW);
-                    ++issued;
+                    tma_load_2d(st + C::W_S, &tmap_s, &w_full[slot], gt.nt * 128, g0);
+                    if (!SYM) tma_load_2d(st + C::W_Z, &tmap_z, &w_full[slot], gt.nt * 128, g0);
+                    used |= 1u << slot;
+                    phases ^= 1u << slot;
                 }
             }
+            // copies in flight land before the CTA leaves
             WaitCtx wd = wc;
             volatile int no_abort = 0;
             wd.abort = &no_abort;
-            Ring d = rw;
-            for (long long k = 0; k < issued && k < C::NW; ++k) {
-                ring_back(d, C::NW);
-                (void)wait_bounded(&w_full[d.idx], d.phase, wd);
-            }
+            for (int i = 0; i < C::NW; ++i)   // parity of a stage's last fill
+                if ((used >> i) & 1u) (void)wait_bounded(&w_full[i], ((phases >> i) & 1u) ^ 1u, wd);
         }
-    } else if (warp == kW16XWarp) {
-        // -------------------------------------- producer: activation ring --
+    } else if (warp == kW16GXWarp) {
+        // ------------------------------------------- producer: activations --
         if (lane == 0) {
-            Ring rx;
-            long long issued = 0;
+            uint32_t phases = 0u, used = 0u;
             bool ok = true;
-            while (ok && walk.next(tile, kb_first, kb_end)) {
+            while (ok && walk.next(tile, u0, u1)) {
                 const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
-                const int boxes = gt.rows > C::XROWS ? 2 : 1;
-                for (int kb = 0; kb < KB; kb += C::KX) {
-                    if (!wait_bounded(&x_empty[rx.idx], rx.phase ^ 1u, wc)) { ok = false; break; }
-                    uint8_t* st = smem + C::OFF_X + rx.idx * C::X_STAGE;
-                    mbar_arrive_expect_tx(&x_full[rx.idx], boxes * (C::KX * C::XROWS * 128));
-                    tma_load_3d(st, &tmap_x, &x_full[rx.idx], 0, gt.row0, kb);
-                    // BN > XROWS only where a stage is one k-block, so the second box follows the first
-                    if (boxes == 2)
-                        tma_load_3d(st + C::XROWS * 128, &tmap_x, &x_full[rx.idx], 0, gt.row0 + C::XROWS, kb);
-                    rx.next(C::NX);
-                    ++issued;
+                // few rows: one or two small boxes per k-block instead of the large ones
+                const bool small = C::XROWS > kW16GSmall && gt.rows <= (BN >= 128 ? 2 : 1) * kW16GSmall;
+                const int per = small ? kW16GSmall : C::XROWS;
+                const int boxes = gt.rows > per ? 2 : 1;
+                const CUtensorMap* map = small ? &tmap_xs : &tmap_x;
+                for (int u = u0; u < u1; ++u) {
+                    const int kb = 2 * u, len = min(2, KB - kb);
+                    const int slot = u & (C::NS - 1);
+                    if (!wait_bounded(&empty[slot], ((phases >> slot) & 1u) ^ 1u, wc)) { ok = false; break; }
+                    uint8_t* st = smem + slot * C::STAGE + 2 * C::A_BYTES;
+                    mbar_arrive_expect_tx(&full[slot], len * boxes * (per * 128));
+                    for (int i = 0; i < len; ++i, st += C::XB) {
+                        tma_load_3d(st, map, &full[slot], 0, gt.row0, kb + i);
+                        if (boxes == 2) tma_load_3d(st + per * 128, map, &full[slot], 0, gt.row0 + per, kb + i);
+                    }
+                    phases ^= 1u << slot;
+                    used |= 1u << slot;
                 }
             }
+            // copies in flight land before the CTA leaves.  A stage completes with its weights; when the CTA gives
+            // up they may never come, and the wait runs to its limit.
             WaitCtx wd = wc;
             volatile int no_abort = 0;
             wd.abort = &no_abort;
-            Ring d = rx;
-            for (long long k = 0; k < issued && k < C::NX; ++k) {
-                ring_back(d, C::NX);
-                (void)wait_bounded(&x_full[d.idx], d.phase, wd);
-            }
+            for (int i = 0; i < C::NS; ++i)
+                if ((used >> i) & 1u) (void)wait_bounded(&full[i], ((phases >> i) & 1u) ^ 1u, wd);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issue --
-        if (lane == 0) {
-            Ring rx, ra, rc;
+        // The whole warp runs the loop and one lane issues: with every value
+        // uniform over the warp, an MMA's descriptors sit in uniform registers
+        // instead of being moved there one by one (135 -> 32 cycles for each).
+        {
+            const bool leader = elect_one();
+            Ring rc;
+            uint32_t phases = 0u;
             bool ok = true;
-            while (ok && walk.next(tile, kb_first, kb_end)) {
+            while (ok && walk.next(tile, u0, u1)) {
                 const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
                 const uint32_t idesc = idesc_bf16((gt.rows + 15) & ~15);
-                if (!wait_bounded(&acc_empty[rc.idx], rc.phase ^ 1u, wc)) { ok = false; break; }
+                if (!warp_wait_bounded(&acc_empty[rc.idx], rc.phase ^ 1u, wc)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + rc.idx * BN;
-                int xo = 0;   // offset of the next k-block in its activation stage
-                for (int kb = 0; kb < KB && ok; kb += C::KA) {
-                    const int len = min(C::KA, KB - kb);
-                    if (!wait_bounded(&a_full[ra.idx], ra.phase, wc)) { ok = false; break; }
+                for (int u = u0; u < u1; ++u) {
+                    const int slot = u & (C::NS - 1);
+                    if (!warp_wait_bounded(&full[slot], (phases >> slot) & 1u, wc)) { ok = false; break; }
                     tc_fence_after();
-                    const uint64_t adesc0 = umma_desc_kmajor(smem_u32(smem + C::OFF_A + ra.idx * C::A_STAGE), 128);
+                    if (leader) {
+                        const uint32_t st = smem_u32(smem + slot * C::STAGE);
+                        const uint64_t adesc = umma_desc_kmajor(st, 128);
+                        const uint64_t bdesc = umma_desc_kmajor(st + 2 * C::A_BYTES, 128);
 #pragma unroll
-                    for (int j = 0; j < C::KA; ++j) {
-                        if (j < len) {
-                            if (xo == 0) {
-                                if (!wait_bounded(&x_full[rx.idx], rx.phase, wc)) { ok = false; break; }
-                                tc_fence_after();
-                            }
-                            const uint64_t adesc = adesc0 + (uint64_t)(j * (C::A_BYTES >> 4));
-                            const uint64_t bdesc =
-                                umma_desc_kmajor(smem_u32(smem + C::OFF_X + rx.idx * C::X_STAGE + xo * C::XB), 128);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_bf16(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, (u > u0 || kk > 0) ? 1u : 0u);
+                        if (2 * u + 1 < KB) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_bf16(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc,
-                                         (kb > 0 || j > 0 || kk > 0) ? 1u : 0u);
-                            if (xo + 1 == C::KX || kb + j + 1 == KB) {
-                                tc_commit(&x_empty[rx.idx]);
-                                rx.next(C::NX);
-                                xo = 0;
-                            } else {
-                                ++xo;
-                            }
+                                mma_bf16(d_tmem, adesc + (C::A_BYTES >> 4) + 2 * kk, bdesc + (C::XB >> 4) + 2 * kk, idesc, 1u);
                         }
+                        tc_commit(&empty[slot]);
                     }
-                    if (!ok) break;
-                    tc_commit(&a_empty[ra.idx]);
-                    ra.next(C::NA);
+                    __syncwarp();
+                    phases ^= 1u << slot;
                 }
                 if (!ok) break;
-                tc_commit(&acc_full[rc.idx]);
+                if (leader) tc_commit(&acc_full[rc.idx]);
+                __syncwarp();
                 rc.next(2);
             }
             // drain: every MMA issued above completes before TMEM is freed
-            tc_commit(drain);
-            WaitCtx wd = wc;
-            volatile int no_abort = 0;
-            wd.abort = &no_abort;
-            (void)wait_bounded(drain, 0, wd);
+            if (leader) {
+                tc_commit(drain);
+                WaitCtx wd = wc;
+                volatile int no_abort = 0;
+                wd.abort = &no_abort;
+                (void)wait_bounded(drain, 0, wd);
+            }
+            __syncwarp();
         }
-    } else if (warp >= kW16DqWarp0 && warp < kW16DqWarp0 + kW16DqWarps) {
+    } else if (warp >= kW16GDqWarp0 && warp < kW16GDqWarp0 + kW16GDqWarps) {
         // ----------------------------------------------------- dequantize --
-        const int dt = threadIdx.x - kW16DqWarp0 * 32;  // 0..255
+        // The teams take k-blocks in turn, so that one's waits and hand-over
+        // overlap the others' arithmetic.  A thread takes one column's 64 k:
+        // they lie in one group, so its scale is set up once for 64 weights.
+        const int dt = threadIdx.x - kW16GDqWarp0 * 32;  // 0..511
+        const int team = dt >> 7;
         const int r = dt & 127;                          // weight column within the tile = A row
-        const int cc = dt >> 7;                          // 32-k chunk of the k-block
         const int hf = r >> 6;
-        const uint32_t row_addr = smem_u32(smem + C::OFF_A) + r * 128;
-        Ring rw, ra;
-        uint64_t A[5], S[5];
+        // unit i of the row lies at row ^ (i << 4) (128-byte swizzle)
+        const uint32_t row0 = smem_u32(smem) + (team & 1) * C::A_BYTES + r * 128 + ((r & 7) << 4);
+        const int j = team & 1;                          // this team's k-block of its pair's two
+        const uint32_t off_c = hf * C::PK_HALF + j * 2048 + (r & 63) * 16;
+        const uint32_t off_s = C::W_S + ((j >> kb_shift) * 128 + r) * 4, off_z = C::W_Z + (j >> kb_shift) * 128 + r;
+        uint32_t phases = 0u, w_phases = 0u;             // of the stages, of those of packed weights
         bool ok = true;
-        while (ok && walk.next(tile, kb_first, kb_end)) {
+        while (ok && walk.next(tile, u0, u1)) {
             const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
             const bool valid = hf * 64 < min(128, p.N - gt.nt * 128);
-            int wo = 0;               // offset of the next k-block in its weight stage
-            int g0 = 0, g_prev = -1;
-            for (int kb = 0; kb < KB; kb += C::KA) {
-                const int len = min(C::KA, KB - kb);
-                if (wo == 0) {
-                    ok = warp_wait_bounded(&w_full[rw.idx], rw.phase, wc);
-                    g0 = kb >> kb_shift;
-                }
-                if (ok) ok = warp_wait_bounded(&a_empty[ra.idx], ra.phase ^ 1u, wc);
+            for (int u = u0 + ((u0 ^ (team >> 1)) & 1); u < u1; u += 2) {   // the pair's stages: u % 2 = team / 2
+                const int slot = u & (C::NW - 1);
+                ok = warp_wait_bounded(&w_full[slot], (w_phases >> slot) & 1u, wc);
                 if (!ok) break;
-                const uint8_t* st = smem + C::OFF_W + rw.idx * C::W_STAGE;
-                uint4 c[C::KA];
-#pragma unroll
-                for (int j = 0; j < C::KA; ++j)
-                    c[j] = (valid && j < len)
-                               ? *reinterpret_cast<const uint4*>(st + hf * C::PK_HALF + (wo + j) * 2048 + cc * 1024 +
-                                                                 (r & 63) * 16)
-                               : make_uint4(0u, 0u, 0u, 0u);
-                uint4 out[C::KA][4];
-#pragma unroll
-                for (int j = 0; j < C::KA; ++j) {
-                    if (valid && j < len) {
-                        const int gi = (kb + j) >> kb_shift;
-                        if (gi != g_prev) {
-                            const float sv = reinterpret_cast<const float*>(st + C::W_S)[(gi - g0) * 128 + r];
-                            const float zc = SYM ? 8.0f : (float)st[C::W_Z + (gi - g0) * 128 + r];
-#pragma unroll
-                            for (int q = 0; q < 5; ++q) {
-                                const float sc = (float)(1 << (4 * q));
-                                A[q] = f2_splat(-(8388608.0f + zc * sc));
-                                S[q] = f2_splat(sv * (1.0f / sc));
-                            }
-                            g_prev = gi;
-                        }
-                        dequant_chunk<SYM>(c[j], A, S, out[j]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) out[j][i] = make_uint4(0u, 0u, 0u, 0u);
-                    }
+                w_phases ^= 1u << slot;
+                // everything this thread needs of the stage, which is then free again
+                const bool mine = 2 * u + j < KB;        // warp-uniform
+                const uint8_t* st = smem + C::OFF_W + slot * C::W_STAGE;
+                uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0;
+                float sv = 0.0f;                         // columns past N: scale 0
+                uint32_t zv = 0u;
+                if (valid && mine) {
+                    c0 = *reinterpret_cast<const uint4*>(st + off_c);
+                    c1 = *reinterpret_cast<const uint4*>(st + off_c + 1024);
+                    sv = *reinterpret_cast<const float*>(st + off_s);
+                    if (!SYM) zv = st[off_z];
                 }
-                wo += len;
-                if (wo == kW16KSW || kb + len == KB) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&w_empty[rw.idx]);
-                    rw.next(C::NW);
-                    wo = 0;
-                }
-                const uint32_t a_row = row_addr + ra.idx * C::A_STAGE;
-#pragma unroll
-                for (int j = 0; j < C::KA; ++j) {
-                    if (j < len) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int jj = cc * 4 + i;
-                            const uint32_t addr = a_row + j * C::A_BYTES + ((jj ^ (r & 7)) << 4);
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(out[j][i].x),
-                                         "r"(out[j][i].y), "r"(out[j][i].z), "r"(out[j][i].w)
-                                         : "memory");
-                        }
-                    }
-                }
-                fence_proxy_async_smem();  // generic-proxy writes -> visible to the tensor core
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&a_full[ra.idx]);
-                ra.next(C::NA);
+                if (lane == 0) mbar_arrive(&w_empty[slot]);
+                uint4 out[8];
+                if (mine) {
+                    NibblePairs<SYM> q;
+                    q.set(sv, zv);
+                    dequant_word32<SYM>(c0.x, q, &out[0].x, &out[2].x);
+                    dequant_word32<SYM>(c0.y, q, &out[0].z, &out[2].z);
+                    dequant_word32<SYM>(c0.z, q, &out[1].x, &out[3].x);
+                    dequant_word32<SYM>(c0.w, q, &out[1].z, &out[3].z);
+                    dequant_word32<SYM>(c1.x, q, &out[4].x, &out[6].x);
+                    dequant_word32<SYM>(c1.y, q, &out[4].z, &out[6].z);
+                    dequant_word32<SYM>(c1.z, q, &out[5].x, &out[7].x);
+                    dequant_word32<SYM>(c1.w, q, &out[5].z, &out[7].z);
+                }
+                const int as = u & (C::NS - 1);
+                ok = warp_wait_bounded(&empty[as], ((phases >> as) & 1u) ^ 1u, wc);
+                if (!ok) break;
+                phases ^= 1u << as;
+                if (mine) {
+                    const uint32_t a_row = row0 + as * C::STAGE;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a_row ^ (i << 4)), "r"(out[i].x),
+                                     "r"(out[i].y), "r"(out[i].z), "r"(out[i].w)
+                                     : "memory");
+                    fence_proxy_async_smem();  // generic-proxy writes -> visible to the tensor core
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[as]);
             }
         }
-    } else if (warp >= kW16EpiWarp0 && warp < kW16EpiWarp0 + 4) {
+    } else if (warp >= kW16GEpiWarp0 && warp < kW16GEpiWarp0 + 4) {
         // ------------------------------------------------------- epilogue --
         const int q = warp & 3;                 // TMEM lane quadrant
         const uint32_t lane_addr = ((uint32_t)(q * 32)) << 16;
-        uint16_t* stg = reinterpret_cast<uint16_t*>(smem + C::OFF_Y) + (warp - kW16EpiWarp0) * 1024;
+        uint16_t* stg = reinterpret_cast<uint16_t*>(smem + C::OFF_Y) + (warp - kW16GEpiWarp0) * (C::STG / 8);
         constexpr int LB = C::LB;
+        const int c_in = q * 32 + lane;         // column within the tile
         Ring ra;
-        while (walk.next(tile, kb_first, kb_end)) {
+        while (walk.next(tile, u0, u1)) {
             const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
-            if (!warp_wait_bounded(&acc_full[ra.idx], ra.phase, wc)) break;
+            bool ok = warp_wait_bounded(&acc_full[ra.idx], ra.phase, wc);
+            if (walk.split) ok = !named_bar_or(1, 128, !ok);  // one decision before the barriers below
+            if (!ok) break;
             tc_fence_after();
             const uint32_t tacc = tmem_base + lane_addr + ra.idx * BN;
             const int col0 = gt.nt * 128 + q * 32;
-            if (col0 < p.N) {
+            const bool live = col0 < p.N;       // warp-uniform
+            bool write = live, parts = false;
+            int nparts = 0, c_first = 0;
+            constexpr long long kTile = (long long)BN * 128;
+            if (walk.split && (u0 > 0 || u1 < p.units)) {
+                // part of a tile: the raw sums go to this CTA's slot (0: the tile began in an earlier CTA)
+                float* dst = p.partial + (2LL * blockIdx.x + (u0 > 0 ? 0 : 1)) * kTile + c_in;
+                if (live) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < gt.rows; c0 += LB) {
+                        uint32_t v[LB];
+                        tmem_ld32<LB>(tacc + c0, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < LB; ++i) dst[(c0 + i) * 128] = __uint_as_float(v[i]);
+                    }
+                }
+                tc_fence_before();
+                const int t0 = (int)tile * p.units;
+                c_first = t0 / walk.Q;
+                nparts = (t0 + p.units - 1) / walk.Q - c_first + 1;
+                named_bar_sync(1, 128);
+                if (threadIdx.x == kW16GEpiWarp0 * 32) {
+                    __threadfence();
+                    *last_flag = count_in(p.counts + tile, p.epoch, nparts) == nparts - 1;
+                    __threadfence();
+                }
+                named_bar_sync(1, 128);
+                write = live && *reinterpret_cast<volatile int*>(last_flag) != 0;
+                parts = true;
+            }
+            if (write) {
 #pragma unroll 1
                 for (int c0 = 0; c0 < gt.rows; c0 += LB) {
                     uint32_t v[LB];
-                    tmem_ld32<LB>(tacc + c0, v);
-                    tmem_wait_ld();
+                    if (parts) {
+                        // in the order of k, whoever came last: the same sum in every run
+#pragma unroll
+                        for (int i = 0; i < LB; ++i) v[i] = 0u;
+#pragma unroll 2
+                        for (int k = 0; k < nparts; ++k) {
+                            const int c = c_first + k;
+                            const int slot = c * walk.Q > (int)tile * p.units ? 0 : 1;
+                            const float* src = p.partial + (2LL * c + slot) * kTile + c0 * 128 + c_in;
+#pragma unroll
+                            for (int i = 0; i < LB; ++i)
+                                v[i] = __float_as_uint(__uint_as_float(v[i]) + __ldcg(src + i * 128));
+                        }
+                    } else {
+                        tmem_ld32<LB>(tacc + c0, v);
+                        tmem_wait_ld();
+                    }
                     __syncwarp();  // the previous batch's copy-out is done with the staging
 #pragma unroll
-                    for (int j = 0; j < LB; ++j) stg[j * 32 + lane] = f32_to_bf16_bits(__uint_as_float(v[j]));
+                    for (int i = 0; i < LB; ++i) stg[i * 32 + lane] = f32_to_bf16_bits(__uint_as_float(v[i]));
                     __syncwarp();
 #pragma unroll
                     for (int i = lane; i < LB * 4; i += 32) {
@@ -383,11 +512,11 @@ __global__ void __launch_bounds__(kW16Threads, 1)
 }
 
 // Launches the grouped W4A16 tile kernel for a tile of BN in {16, 32, 64, 128,
-// 256} rows (defined in gemm_w4a16_grouped.cu).  Status codes as in w4a8.h.
-int launch_w4a16_grouped(int bn, bool sym, const CUtensorMap& tmap_x, const CUtensorMap& tmap_s,
-                         const CUtensorMap& tmap_z, const W16GroupedParams& p, int grid, cudaStream_t stream);
+// 224} rows (defined in gemm_w4a16_grouped.cu).  tmap_xs: boxes of kW16GSmall
+// rows x one k-block.  Status codes as in w4a8.h.
+int launch_w4a16_grouped(int bn, bool sym, const CUtensorMap& tmap_x, const CUtensorMap& tmap_xs,
+                         const CUtensorMap& tmap_s, const CUtensorMap& tmap_z, const W16GroupedParams& p, int grid,
+                         cudaStream_t stream);
 
-// Rows of one activation request of a tile of bn rows.
-inline int w4a16_grouped_xrows(int bn) { return bn < 128 ? bn : 128; }
 
 }  // namespace w4a8

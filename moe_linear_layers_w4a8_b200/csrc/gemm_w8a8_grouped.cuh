@@ -90,6 +90,7 @@ struct W8GCfg {
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int ACC_COLS = 4 * BN;                 // two pairs of accumulators
     static constexpr uint32_t TMEM_COLS = ACC_COLS;
+    static constexpr int SPLIT_GAIN = 4 + BN / 16;          // k-blocks of 128 (a partial tile is BN KB)
     static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128, "BN");
     static_assert(NST >= 3, "stages");
     static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -155,13 +156,14 @@ struct GroupedWalk {
     int u, u1, Q, KB;            // split: unit range
     bool split;
 
-    __device__ __forceinline__ GroupedWalk(const GroupTable& g, int E, int n_tiles, int KB_, int split_tiles) {
+    // Split where that shortens the longest CTA's work by at least `gain` units:
+    // less does not pay for the partial tiles.
+    __device__ __forceinline__ GroupedWalk(const GroupTable& g, int E, int n_tiles, int KB_, int split_tiles, int gain) {
         KB = KB_;
         tiles = (long long)g.mt[E] * n_tiles;
         const long long grid = gridDim.x;
         const long long waves = (tiles + grid - 1) / grid;
-        // more than 15% of the CTAs idle in the last wave
-        split = tiles < split_tiles && KB > 1 && 20 * tiles < 17 * waves * grid;
+        split = tiles < split_tiles && waves * KB - (tiles * KB + grid - 1) / grid >= gain;
         t = blockIdx.x;
         Q = 0;
         u = u1 = 0;
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const WaitCtx wc{abort_flag, p.status, wait_cycles_for_ns(p.wait_ns)};
-    GroupedWalk walk(g, p.E, p.n_tiles, p.KB, p.split_tiles);
+    GroupedWalk walk(g, p.E, p.n_tiles, p.KB, p.split_tiles, C::SPLIT_GAIN);
     long long tile;
     int kb0, kb1;
 
@@ -326,22 +328,26 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issue --
-        if (lane == 0) {
-            Ring rs, ra;
-            bool ok = true;
-            while (ok && walk.next(tile, kb0, kb1)) {
-                const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
-                const uint32_t idesc = idesc_i8((gt.rows + 15) & ~15);
-                const bool two = GATEUP || p.N - gt.nt * 256 > 128;
-                if (!wait_bounded(&acc_empty[ra.idx], ra.phase ^ 1u, wc)) { ok = false; break; }
+        // The whole warp runs the loop and one lane issues: with every value
+        // uniform over the warp, an MMA's descriptors sit in uniform registers
+        // instead of being moved there one by one (measured in the W4A16
+        // kernel: 135 -> 32 cycles for each MMA).
+        const bool leader = elect_one();
+        Ring rs, ra;
+        bool ok = true;
+        while (ok && walk.next(tile, kb0, kb1)) {
+            const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
+            const uint32_t idesc = idesc_i8((gt.rows + 15) & ~15);
+            const bool two = GATEUP || p.N - gt.nt * 256 > 128;
+            ok = warp_wait_bounded(&acc_empty[ra.idx], ra.phase ^ 1u, wc);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d0 = tmem_base + ra.idx * (2 * BN);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = warp_wait_bounded(&w_full[rs.idx], rs.phase, wc) && warp_wait_bounded(&x_full[rs.idx], rs.phase, wc);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t d0 = tmem_base + ra.idx * (2 * BN);
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!wait_bounded(&w_full[rs.idx], rs.phase, wc) || !wait_bounded(&x_full[rs.idx], rs.phase, wc)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                if (leader) {
                     const uint32_t a_addr = smem_u32(smem + rs.idx * C::STAGE);
                     const uint64_t adesc = umma_desc_kmajor(a_addr, 128);
                     const uint64_t bdesc = umma_desc_kmajor(a_addr + C::A_STAGE, 128);
@@ -352,19 +358,24 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
                         if (two) mma_i8(d0 + BN, adesc + (128 * 128 >> 4) + 2 * kk, bdesc + 2 * kk, idesc, acc);
                     }
                     tc_commit(&empty[rs.idx]);
-                    rs.next(C::NST);
                 }
-                if (!ok) break;
-                tc_commit(&acc_full[ra.idx]);
-                ra.next(2);
+                __syncwarp();
+                rs.next(C::NST);
             }
-            // drain: every MMA issued above completes before TMEM is freed
+            if (!ok) break;
+            if (leader) tc_commit(&acc_full[ra.idx]);
+            __syncwarp();
+            ra.next(2);
+        }
+        // drain: every MMA issued above completes before TMEM is freed
+        if (leader) {
             tc_commit(drain);
             WaitCtx wd = wc;
             volatile int no_abort = 0;
             wd.abort = &no_abort;
             (void)wait_bounded(drain, 0, wd);
         }
+        __syncwarp();
     } else {
         // ------------------------------------------------------- epilogue --
         const int q = warp & 3;                          // TMEM lane quadrant
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
                         const long long tile_ints = 2LL * BN * 128;
 #pragma unroll
                         for (int j = 0; j < LB; ++j) v[j] = 0u;
-#pragma unroll 1
+#pragma unroll 2
                         for (int k = 0; k < nparts; ++k) {
                             const int c = c_first + k;
                             const int slot = c * walk.Q > (int)tile * p.KB ? 0 : 1;

@@ -485,6 +485,17 @@ __device__ __forceinline__ bool warp_wait_bounded(uint64_t* bar, uint32_t parity
     return __all_sync(0xFFFFFFFFu, ok) != 0;
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Position of a unit: k-block kb of the virtual tile t, which is the real
 // tile ta = base + (t - v0) * stride (stride 1, base = v0 = 0 for a
 // contiguous range; stride = the grid size for tiles handed out round-robin),

@@ -497,13 +497,31 @@ struct W8GroupedPlan {
     size_t counts_off, ws_bytes;
 };
 
+// Tile height out of `sizes` (descending): the largest whose tiles should fill
+// the grid, taking min(E, R) + R / bn m-tiles for ragged rows, and whose next
+// smaller one is less than `tall` times the mean rows of an expert; where even
+// the smallest does not fill it, one that holds the mean rows (at most 64).
+int grouped_bn(long long R, int E, int n_tiles, int grid, const int* sizes, int n, int tall) {
+    const long long busy = std::max<long long>(1, std::min<long long>(E, R));
+    for (int i = 0; i < n; ++i)
+        if ((busy + R / sizes[i]) * n_tiles >= grid && (i == n - 1 || sizes[i + 1] * busy < tall * R)) return sizes[i];
+    const long long mean = (R + busy - 1) / busy;
+    for (int i = n - 1; i >= 0; --i)
+        if (sizes[i] >= mean || sizes[i] >= 64) return sizes[i];
+    return sizes[0];
+}
+
 W8GroupedPlan plan_w8_grouped(long long R, int E, int N, int K, bool gate_up, int sms) {
     W8GroupedPlan pl{};
-    pl.bn = pick_bn((R + E - 1) / E);
     const int cols = gate_up ? 128 : 256;
     pl.n_tiles = (N + cols - 1) / cols;
     pl.KB = K / 128;
     pl.grid = sms <= 0 ? 1 : (sms > 254 ? 254 : sms);  // arrivals are counted in 8 bits
+    const int sizes[4] = {128, 64, 32, 16};
+    // Few rows: the smaller a tile, the deeper the ring of weight stages.  512
+    // rows over 32 uneven experts: 16, 32, 64, 128 rows 172, 164, 177, 175 us;
+    // 741 rows over 8 of 11, N = 1040: 11.8, 8.5, 9.5, 11.5 us.
+    pl.bn = grouped_bn(R, E, pl.n_tiles, pl.grid, sizes, 4, 2);
     const long long fewest = ((R + pl.bn - 1) / pl.bn) * pl.n_tiles;
     if (pl.KB > 1 && fewest < 4LL * pl.grid) {
         pl.split_tiles = 4 * pl.grid;
@@ -701,18 +719,39 @@ w4a8_status w16_gemm_impl(const uint16_t* X, int M, int ldx, const uint8_t* pack
                                                  static_cast<cudaStream_t>(stream)));
 }
 
+// Launch plan of a grouped W4A16 GEMM, as for the W8A8 one: units of two
+// k-blocks of 64, fp32 partial tiles of 128 columns.
+W8GroupedPlan plan_w16_grouped(long long R, int E, int N, int K, int sms) {
+    W8GroupedPlan pl{};
+    pl.n_tiles = (N + 127) / 128;
+    pl.KB = (K / 64 + 1) / 2;
+    pl.grid = sms <= 0 ? 1 : (sms > 254 ? 254 : sms);
+    const int sizes[5] = {224, 128, 64, 32, 16};
+    // A taller tile dequantizes a weight fewer times.  512 rows over 32 uneven
+    // experts: 16, 64, 128, 224 rows 443, 293, 287, 259 us; 777 rows over 8 of
+    // 10, N = 1088: 32.9, 14.0, 14.8, 16.2 us; 6 experts of one row: 15.2, 16.7,
+    // 16.3, 16.1 us.
+    pl.bn = grouped_bn(R, E, pl.n_tiles, pl.grid, sizes, 5, 16);
+    const long long fewest = ((R + pl.bn - 1) / pl.bn) * pl.n_tiles;
+    if (pl.KB > 1 && fewest < 4LL * pl.grid) {
+        pl.split_tiles = 4 * pl.grid;
+        pl.counts_off = (size_t)2 * pl.grid * pl.bn * 128 * sizeof(float);
+        pl.ws_bytes = pl.counts_off + (size_t)pl.split_tiles * sizeof(unsigned long long);
+    }
+    return pl;
+}
+
 // The grouped W4A16 product.
 w4a8_status launch_w16_grouped(const uint16_t* X, int ldx, const int32_t* offsets, int R, int E,
                                const uint8_t* packed, const float* s_w, const uint8_t* z, const w4a8_wdesc* w,
-                               uint16_t* Y, int ldy, int32_t* dev_status, cudaStream_t s) {
-    const int sms = sm_count_current();
-    const long long mean = ((long long)R + E - 1) / E;
-    const int bn = mean > 128 ? 256 : pick_bn(mean);
-    const int G = w->K / w->group;
-    // scale / zero-point rows of one weight stage of 8 k-blocks (stages start at multiples of 8)
-    const int sg_rows = w->group == 64 ? 8 : 4;
-    CUtensorMap tx, ts, tz;
-    if (!make_bf16_k64_tmap(&tx, X, R, w->K, ldx, w4a16_grouped_xrows(bn), w16_box_kb(bn)) ||
+                               uint16_t* Y, int ldy, void* workspace, int32_t* dev_status, cudaStream_t s) {
+    const W8GroupedPlan pl = plan_w16_grouped(R, E, w->N, w->K, sm_count_current());
+    const int bn = pl.bn, G = w->K / w->group;
+    // scale / zero-point rows of one weight stage (a whole number of groups from its first k on)
+    const int sg_rows = 64 * kW16GKSW / w->group;
+    CUtensorMap tx, txs, ts, tz;
+    if (!make_bf16_k64_tmap(&tx, X, R, w->K, ldx, w4a16_grouped_xrows(bn), 1) ||
+        !make_bf16_k64_tmap(&txs, X, R, w->K, ldx, kW16GSmall, 1) ||
         !make_group_tmap(&ts, s_w, E * G, w->N, true, sg_rows))
         return W4A8_ERR_CUDA;
     if (z) {
@@ -728,18 +767,24 @@ w4a8_status launch_w16_grouped(const uint16_t* X, int ldx, const int32_t* offset
     p.R = R;
     p.G = G;
     p.group = w->group;
-    p.n_tiles = (w->N + 127) / 128;
+    p.n_tiles = pl.n_tiles;
+    p.units = pl.KB;
     p.offsets = offsets;
     p.packed = packed;
     p.packed_estride = (long long)w->K * w->N / 2;
-    p.sg_rows = sg_rows;
     p.Y = Y;
     p.ldy = ldy;
     p.vec16 = (aligned16(Y) && ldy % 8 == 0) ? 1 : 0;
+    p.split_tiles = pl.split_tiles;
+    if (pl.split_tiles > 0) {
+        p.partial = static_cast<float*>(workspace);
+        p.counts = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + pl.counts_off);
+        p.epoch = next_epoch();
+    }
     p.status = dev_status;
     p.wait_ns = kDefaultWaitNs;
     return static_cast<w4a8_status>(
-        launch_w4a16_grouped(bn, w->symmetric != 0, tx, ts, tz, p, sms <= 0 ? 1 : sms, s));
+        launch_w4a16_grouped(bn, w->symmetric != 0, tx, txs, ts, tz, p, pl.grid, s));
 }
 
 }  // namespace
@@ -1170,21 +1215,33 @@ w4a8_status w4a16_gemm(const uint16_t* X, int M, int ldx, const uint8_t* packed,
     return w16_gemm_impl(X, M, ldx, packed, s_w, z, w, Y, ldy, workspace, ws_bytes, dev_status, stream);
 }
 
-w4a8_status w4a16_grouped_gemm(const uint16_t* X, int R, int ldx, const int32_t* offsets, int E,
-                               const uint8_t* packed, const float* s_w, const uint8_t* z, const w4a8_wdesc* w,
-                               uint16_t* Y, int ldy, int32_t* dev_status, void* stream) {
-    w4a8_status st = check_wdesc(w);
+static w4a8_status check_w16_grouped(int R, int E, const w4a8_wdesc* w) {
+    const w4a8_status st = check_wdesc(w);
     if (st != W4A8_OK) return st;
     if (R < 0 || E <= 0) return W4A8_ERR_INVALID_ARG;
-    if (E > kGroupedMaxExperts || R > (1 << 24) || w->K > (1 << 24) ||
-        (long long)E * (w->K / w->group) > (1ll << 30))
-        return W4A8_ERR_UNSUPPORTED_SHAPE;
+    if (E > kGroupedMaxExperts || R > (1 << 24) || w->K > (1 << 17)) return W4A8_ERR_UNSUPPORTED_SHAPE;
+    return W4A8_OK;
+}
+
+size_t w4a16_grouped_workspace_size(int R, int E, const w4a8_wdesc* w) {
+    if (check_w16_grouped(R, E, w) != W4A8_OK || R == 0) return 0;
+    return plan_w16_grouped(R, E, w->N, w->K, sm_count_current()).ws_bytes;
+}
+
+w4a8_status w4a16_grouped_gemm(const uint16_t* X, int R, int ldx, const int32_t* offsets, int E,
+                               const uint8_t* packed, const float* s_w, const uint8_t* z, const w4a8_wdesc* w,
+                               uint16_t* Y, int ldy, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                               void* stream) {
+    const w4a8_status st = check_w16_grouped(R, E, w);
+    if (st != W4A8_OK) return st;
     if (R == 0) return W4A8_OK;
     if (!X || !offsets || !packed || !s_w || !Y || ldx < w->K || ldy < w->N) return W4A8_ERR_INVALID_ARG;
     if (w->symmetric ? (z != nullptr) : (z == nullptr)) return W4A8_ERR_FORMAT_MISMATCH;
     if (!aligned16(X) || ldx % 8 != 0 || !aligned16(packed) || !aligned16(s_w) || (z && !aligned16(z)))
         return W4A8_ERR_INVALID_ARG;
-    return launch_w16_grouped(X, ldx, offsets, R, E, packed, s_w, z, w, Y, ldy, dev_status,
+    const size_t need = w4a16_grouped_workspace_size(R, E, w);
+    if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return W4A8_ERR_WORKSPACE;
+    return launch_w16_grouped(X, ldx, offsets, R, E, packed, s_w, z, w, Y, ldy, workspace, dev_status,
                               static_cast<cudaStream_t>(stream));
 }
 

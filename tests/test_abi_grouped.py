@@ -126,11 +126,13 @@ def test_binding_refusals():
     (dict(Y=None), 1), (dict(pk=None), 1), (dict(pk=ODD), 1), (dict(sw=None), 1), (dict(sw=ODD), 1),
     (dict(z=FAKE), 3), (dict(sym=0), 3), (dict(bits=8), 3), (dict(group=32), 3), (dict(N=500), 3),
     (dict(R=-1), 1), (dict(E=0), 1), (dict(E=513), 2), (dict(R=(1 << 24) + 1), 2), (dict(R=0), 0),
+    (dict(N=128, ws=None), 7), (dict(N=128, ws=ODD), 7), (dict(N=128, wsb=100), 7),
 ])
 def test_w4a16_grouped_refusals(lib, kw, code):
     import moe_linear_layers_w4a8_b200 as m
-    a = dict(X=FAKE, R=16, ldx=512, off=FAKE, E=4, pk=FAKE, sw=FAKE, z=None, Y=FAKE, ldy=512, sym=1, bits=4, group=128, N=512)
+    a = dict(X=FAKE, R=16, ldx=512, off=FAKE, E=4, pk=FAKE, sw=FAKE, z=None, Y=FAKE, ldy=512, sym=1, bits=4, group=128,
+             N=512, ws=FAKE, wsb=BIG)
     a.update(kw)
     d = m.WDesc(a["bits"], a["sym"], a["group"], 512, a["N"], 1)
     assert lib.w4a16_grouped_gemm(a["X"], a["R"], a["ldx"], a["off"], a["E"], a["pk"], a["sw"], a["z"],
-                                  ctypes.byref(d), a["Y"], a["ldy"], None, None) == code
+                                  ctypes.byref(d), a["Y"], a["ldy"], a["ws"], a["wsb"], None, None) == code

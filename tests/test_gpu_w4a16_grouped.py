@@ -168,6 +168,27 @@ def test_nonfinite_rows_stay_in_their_row(m):
         assert torch.isnan(got[1]).all() and not torch.isfinite(got[R - 2]).any()
 
 
+def test_workspace_contents_and_order_do_not_matter(m):
+    """Split launches: a workspace full of anything, reused by other shapes,
+    gives the same bits every time."""
+    shapes = [([1, 1, 2, 1], 2048, 512), ([5, 0, 90, 1], 1024, 192), ([16] * 4, 1216, 640), ([200], 4096, 64)]
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    todo = []
+    for counts, K, N in shapes:
+        w, _ = _weights(m, len(counts), K, N, 64, False, seed=K)
+        X = torch.randn(sum(counts), K, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+        assert 0 < m.w4a16_grouped_workspace_size(sum(counts), w) <= ws.numel()
+        todo.append((X, _offsets(counts), w, m.w4a16_grouped_gemm(X, _offsets(counts), w).clone()))
+    for fill in (0, 255, None):
+        if fill is None:
+            ws.random_(0, 256, generator=torch.Generator(device="cuda").manual_seed(9))
+        else:
+            ws.fill_(fill)
+        for _ in range(20):
+            for X, off, w, want in todo:
+                assert torch.equal(m.w4a16_grouped_gemm(X, off, w, workspace=ws), want)
+
+
 def test_captured_with_changing_offsets(m):
     w, _ = _weights(m, 4, 512, 256, 128, True, seed=8)
     X = torch.randn(48, 512, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
