@@ -86,6 +86,8 @@ def library_path() -> str:
 def load_library():
     """Loads libw4a8.so (raises W4A8Error(6) when it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -667,9 +669,8 @@ def _launch(dev: torch.device, where: str, fn, *args):
         raise W4A8Error(code, where)
 
 
-def _arg(ok: bool, what: str):
-    if not ok:
-        raise W4A8Error(1, what)
+def _refuse(where: str, what: str):
+    raise W4A8Error(1, f"{where}: {what}")
 
 
 def _scratch(workspace: Optional[torch.Tensor], need: int, dev: torch.device):
@@ -684,38 +685,41 @@ def _scratch(workspace: Optional[torch.Tensor], need: int, dev: torch.device):
     return workspace.data_ptr(), need, workspace
 
 
-def _check_grouped(where: str, x, offsets, w, out, status):
-    """The shape and device rules every grouped product shares; returns (R, K, out)."""
-    _arg(x.is_cuda and x.dim() == 2, f"{where}: rows must be a CUDA matrix [R, K]")
-    dev = x.device
-    E = w.experts
-    _arg(E > 0, f"{where} takes stacked expert weights")
+def _check_status(where: str, status, dev):
+    if status is not None and (status.dtype != torch.int32 or status.device != dev):
+        _refuse(where, f"status must be int32 on {dev}")
+
+
+def _check_grouped(where: str, x, dtype, offsets, w, out, status):
+    """The shape and device rules every grouped product shares; returns
+    (device, rows, row pitch of x, out, row pitch of out)."""
+    if not x.is_cuda or x.dim() != 2 or x.dtype != dtype or x.stride(1) != 1:
+        _refuse(where, f"rows must be a {dtype} matrix [R, K] with unit column stride on a CUDA device")
+    dev, E, N = x.device, w.experts, w.desc.N
+    if E <= 0:
+        _refuse(where, "takes stacked expert weights")
     R, K = x.shape
-    _arg(K == w.desc.K, f"{where}: rows have {K} columns, the weight {w.desc.K} rows")
-    _arg(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.numel() == E + 1 and offsets.is_contiguous()
-         and offsets.device == dev, f"{where}: offsets must be contiguous int32 [E + 1] on {dev}")
+    if K != w.desc.K:
+        _refuse(where, f"rows have {K} columns, the weight {w.desc.K} rows")
+    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or offsets.device != dev or not offsets.is_contiguous():
+        _refuse(where, f"offsets must be contiguous int32 [E + 1] on {dev}")
     if out is None:
-        out = torch.empty(R, w.desc.N, dtype=torch.bfloat16, device=dev)
+        out, pitch = torch.empty(R, N, dtype=torch.bfloat16, device=dev), N
     else:
-        _arg(out.dtype == torch.bfloat16 and out.shape == (R, w.desc.N) and out.device == dev
-             and (out.stride(1) == 1 or w.desc.N == 1) and (out.stride(0) >= w.desc.N or R <= 1),
-             f"{where}: out must be bf16 [R, N] with unit column stride on {dev}")
-    _arg(status is None or (status.dtype == torch.int32 and status.device == dev),
-         f"{where}: status must be int32 on {dev}")
-    return R, K, out
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    """Row pitch of a matrix with unit column stride (a one-row matrix may carry any stride)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+        # a one-row matrix may carry any row stride
+        pitch = out.stride(0) if R > 1 and out.dim() == 2 else N
+        if out.dtype != torch.bfloat16 or out.shape != (R, N) or out.device != dev or out.stride(1) != 1 or pitch < N:
+            _refuse(where, f"out must be bf16 [R, N] with unit column stride on {dev}")
+    _check_status(where, status, dev)
+    return dev, R, x.stride(0) if R > 1 else K, out, pitch
 
 
 def _check_w8(where: str, w: PackedW8, dev):
-    E, d = w.experts, w.desc
-    _arg(w.q_w.dtype == torch.int8 and tuple(w.q_w.shape) == (E, d.N, d.K) and w.q_w.is_contiguous()
-         and w.q_w.device == dev, f"{where}: q_w must be contiguous int8 [E, N, K] on {dev}")
-    _arg(w.s_w.dtype == torch.float32 and tuple(w.s_w.shape) == (E, d.N) and w.s_w.is_contiguous()
-         and w.s_w.device == dev, f"{where}: s_w must be contiguous fp32 [E, N] on {dev}")
+    q, s, d, E = w.q_w, w.s_w, w.desc, w.experts
+    if q.dtype != torch.int8 or q.shape != (E, d.N, d.K) or not q.is_contiguous() or q.device != dev:
+        _refuse(where, f"q_w must be contiguous int8 [E, N, K] on {dev}")
+    if s.dtype != torch.float32 or s.shape != (E, d.N) or not s.is_contiguous() or s.device != dev:
+        _refuse(where, f"s_w must be contiguous fp32 [E, N] on {dev}")
 
 
 def w8a8_grouped_workspace_size(R: int, w: PackedW8) -> int:
@@ -730,17 +734,17 @@ def w8a8_grouped_gemm(qx: torch.Tensor, s_x: torch.Tensor, offsets: torch.Tensor
     [E + 1] stays on the device.  Rows that belong to no expert are left as
     they are in `out` (uninitialised when `out` is not given)."""
     L = load_library()
-    R, _, out = _check_grouped("w8a8_grouped_gemm", qx, offsets, w, out, status)
-    dev = qx.device
-    _arg(qx.dtype == torch.int8 and qx.is_contiguous(), "w8a8_grouped_gemm: qx must be contiguous int8 [R, K]")
-    _arg(s_x.dtype == torch.float32 and s_x.numel() == R and s_x.is_contiguous() and s_x.device == dev,
-         f"w8a8_grouped_gemm: s_x must be contiguous fp32 [R] on {dev}")
-    _check_w8("w8a8_grouped_gemm", w, dev)
+    where = "w8a8_grouped_gemm"
+    dev, R, pitch, out, ldy = _check_grouped(where, qx, torch.int8, offsets, w, out, status)
+    if pitch != w.desc.K:
+        _refuse(where, "qx must be contiguous")
+    if s_x.dtype != torch.float32 or s_x.numel() != R or not s_x.is_contiguous() or s_x.device != dev:
+        _refuse(where, f"s_x must be contiguous fp32 [R] on {dev}")
+    _check_w8(where, w, dev)
     d = ctypes.byref(w.desc)
     ws, ws_bytes, _keep = _scratch(workspace, L.w8a8_grouped_workspace_size(R, w.experts, d), dev)
-    _launch(dev, "w8a8_grouped_gemm", L.w8a8_grouped_gemm, qx.data_ptr(), s_x.data_ptr(), offsets.data_ptr(), R,
-            w.experts, w.q_w.data_ptr(), w.s_w.data_ptr(), d, out.data_ptr(), _row_stride(out), ws, ws_bytes,
-            _addr(status))
+    _launch(dev, where, L.w8a8_grouped_gemm, qx.data_ptr(), s_x.data_ptr(), offsets.data_ptr(), R, w.experts,
+            w.q_w.data_ptr(), w.s_w.data_ptr(), d, out.data_ptr(), ldy, ws, ws_bytes, _addr(status))
     return out
 
 
@@ -755,16 +759,13 @@ def w8a8_grouped_linear(X: torch.Tensor, offsets: torch.Tensor, w: PackedW8, out
     quantization, then the grouped product, in one library call.  Rows that
     belong to no expert are not read."""
     L = load_library()
-    R, _, out = _check_grouped("w8a8_grouped_linear", X, offsets, w, out, status)
-    dev = X.device
-    _arg(X.dtype == torch.bfloat16 and X.stride(1) == 1,
-         "w8a8_grouped_linear: X must be bf16 [R, K] with unit column stride")
-    _check_w8("w8a8_grouped_linear", w, dev)
+    where = "w8a8_grouped_linear"
+    dev, R, pitch, out, ldy = _check_grouped(where, X, torch.bfloat16, offsets, w, out, status)
+    _check_w8(where, w, dev)
     d = ctypes.byref(w.desc)
     ws, ws_bytes, _keep = _scratch(workspace, L.w8a8_grouped_linear_workspace_size(R, w.experts, d), dev)
-    _launch(dev, "w8a8_grouped_linear", L.w8a8_grouped_linear, X.data_ptr(), R, _row_stride(X), offsets.data_ptr(),
-            w.experts, w.q_w.data_ptr(), w.s_w.data_ptr(), d, out.data_ptr(), _row_stride(out), ws, ws_bytes,
-            _addr(status))
+    _launch(dev, where, L.w8a8_grouped_linear, X.data_ptr(), R, pitch, offsets.data_ptr(), w.experts,
+            w.q_w.data_ptr(), w.s_w.data_ptr(), d, out.data_ptr(), ldy, ws, ws_bytes, _addr(status))
     return out
 
 
@@ -781,20 +782,20 @@ def w4a16_grouped_gemm(X: torch.Tensor, offsets: torch.Tensor, w: PackedWeight, 
     no expert are left as they are in `out`."""
     L = load_library()
     where = "w4a16_grouped_gemm"
-    R, _, out = _check_grouped(where, X, offsets, w, out, status)
-    dev, E, d = X.device, w.experts, w.desc
-    _arg(X.dtype == torch.bfloat16 and X.stride(1) == 1, f"{where}: X must be bf16 [R, K] with unit column stride")
-    groups = (E, d.K // d.group, d.N) if d.group > 0 else None
-    _arg(w.packed.dtype == torch.uint8 and w.packed.numel() == E * d.K * d.N // 2 and w.packed.is_contiguous()
-         and w.packed.device == dev, f"{where}: packed must be contiguous uint8 [E, K * N / 2] on {dev}")
-    _arg(w.s_w.dtype == torch.float32 and tuple(w.s_w.shape) == groups and w.s_w.is_contiguous()
-         and w.s_w.device == dev, f"{where}: s_w must be contiguous fp32 [E, G, N] on {dev}")
-    _arg(w.z is None or (w.z.dtype == torch.uint8 and tuple(w.z.shape) == groups and w.z.is_contiguous()
-                         and w.z.device == dev), f"{where}: z must be contiguous uint8 [E, G, N] on {dev}")
-    ws, ws_bytes, _keep = _scratch(workspace, L.w4a16_grouped_workspace_size(R, E, ctypes.byref(d)), dev)
-    _launch(dev, where, L.w4a16_grouped_gemm, X.data_ptr(), R, _row_stride(X), offsets.data_ptr(), E,
-            w.packed.data_ptr(), w.s_w.data_ptr(), _addr(w.z), ctypes.byref(d), out.data_ptr(), _row_stride(out), ws,
-            ws_bytes, _addr(status))
+    dev, R, pitch, out, ldy = _check_grouped(where, X, torch.bfloat16, offsets, w, out, status)
+    E, d, packed, s_w, z = w.experts, w.desc, w.packed, w.s_w, w.z
+    groups = (E, d.K // d.group if d.group > 0 else 0, d.N)
+    if (packed.dtype != torch.uint8 or packed.numel() != E * d.K * d.N // 2 or not packed.is_contiguous()
+            or packed.device != dev):
+        _refuse(where, f"packed must be contiguous uint8 [E, K * N / 2] on {dev}")
+    if s_w.dtype != torch.float32 or s_w.shape != groups or not s_w.is_contiguous() or s_w.device != dev:
+        _refuse(where, f"s_w must be contiguous fp32 [E, G, N] on {dev}")
+    if z is not None and (z.dtype != torch.uint8 or z.shape != groups or not z.is_contiguous() or z.device != dev):
+        _refuse(where, f"z must be contiguous uint8 [E, G, N] on {dev}")
+    d = ctypes.byref(d)
+    ws, ws_bytes, _keep = _scratch(workspace, L.w4a16_grouped_workspace_size(R, E, d), dev)
+    _launch(dev, where, L.w4a16_grouped_gemm, X.data_ptr(), R, pitch, offsets.data_ptr(), E, packed.data_ptr(),
+            s_w.data_ptr(), _addr(z), d, out.data_ptr(), ldy, ws, ws_bytes, _addr(status))
     return out
 
 
@@ -812,23 +813,22 @@ def w8a8_moe_grouped_gemm(X: torch.Tensor, logits: torch.Tensor, topk: int, w1: 
     Returns dict(out, topk_idx, topk_w, expert_offsets, workspace)."""
     L = load_library()
     where = "w8a8_moe_grouped_gemm"
-    _arg(X.is_cuda and X.dim() == 2 and logits.dim() == 2 and X.dtype == torch.bfloat16
-         and logits.dtype == torch.float32 and logits.device == X.device and logits.shape[0] == X.shape[0],
-         f"{where}: X must be bf16 [T, H] and logits fp32 [T, E] on one CUDA device")
     dev = X.device
+    if (not X.is_cuda or X.dim() != 2 or logits.dim() != 2 or X.dtype != torch.bfloat16
+            or logits.dtype != torch.float32 or logits.device != dev or logits.shape[0] != X.shape[0]):
+        _refuse(where, "X must be bf16 [T, H] and logits fp32 [T, E] on one CUDA device")
     T, H = X.shape
     E, topk = logits.shape[1], int(topk)
-    _arg(w1.experts == E and w2.experts == E and w1.desc.K == H, f"{where}: w1 and w2 must stack E experts for H")
+    if w1.experts != E or w2.experts != E or w1.desc.K != H:
+        _refuse(where, "w1 and w2 must stack E experts for H")
     _check_w8(where, w1, dev)
     _check_w8(where, w2, dev)
-    _arg(status is None or (status.dtype == torch.int32 and status.device == dev),
-         f"{where}: status must be int32 on {dev}")
+    _check_status(where, status, dev)
     X, logits = X.contiguous(), logits.contiguous()
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
-    else:
-        _arg(out.dtype == torch.bfloat16 and out.shape == (T, H) and out.is_contiguous() and out.device == dev,
-             f"{where}: out must be contiguous bf16 [T, H] on {dev}")
+    elif out.dtype != torch.bfloat16 or out.shape != (T, H) or not out.is_contiguous() or out.device != dev:
+        _refuse(where, f"out must be contiguous bf16 [T, H] on {dev}")
     idx = torch.empty(T, max(topk, 0), dtype=torch.int32, device=dev)
     pw = torch.empty(T, max(topk, 0), dtype=torch.float32, device=dev)
     offs = torch.empty(E + 1, dtype=torch.int32, device=dev)
@@ -848,21 +848,23 @@ def w8a8_moe_experts(X: torch.Tensor, expert_ids: torch.Tensor, w1: PackedW8, w2
     """y bf16 [R, H]: row r of X bf16 [R, H] through INT8 expert expert_ids[r] (unweighted)."""
     L = load_library()
     where = "w8a8_moe_experts"
-    _arg(X.is_cuda and X.dim() == 2 and X.dtype == torch.bfloat16, f"{where}: X must be bf16 [R, H] on a CUDA device")
     dev = X.device
+    if not X.is_cuda or X.dim() != 2 or X.dtype != torch.bfloat16:
+        _refuse(where, "X must be bf16 [R, H] on a CUDA device")
     R, H = X.shape
     E = w1.experts
-    _arg(expert_ids.device == dev and expert_ids.numel() == R and not expert_ids.dtype.is_floating_point,
-         f"{where}: expert_ids must be R integers on {dev}")
-    _arg(E > 0 and w2.experts == E and w1.desc.K == H, f"{where}: w1 and w2 must stack the same experts for H")
+    if expert_ids.device != dev or expert_ids.numel() != R or expert_ids.dtype.is_floating_point:
+        _refuse(where, f"expert_ids must be R integers on {dev}")
+    if E <= 0 or w2.experts != E or w1.desc.K != H:
+        _refuse(where, "w1 and w2 must stack the same experts for H")
     _check_w8(where, w1, dev)
     _check_w8(where, w2, dev)
+    _check_status(where, status, dev)
     X, ids = X.contiguous(), expert_ids.to(torch.int32).contiguous()
     if out is None:
         out = torch.empty(R, H, dtype=torch.bfloat16, device=dev)
-    else:
-        _arg(out.dtype == torch.bfloat16 and out.shape == (R, H) and out.is_contiguous() and out.device == dev,
-             f"{where}: out must be contiguous bf16 [R, H] on {dev}")
+    elif out.dtype != torch.bfloat16 or out.shape != (R, H) or not out.is_contiguous() or out.device != dev:
+        _refuse(where, f"out must be contiguous bf16 [R, H] on {dev}")
     d1, d2 = ctypes.byref(w1.desc), ctypes.byref(w2.desc)
     ws, ws_bytes, _keep = _scratch(workspace, L.w8a8_moe_experts_workspace_size(R, E, d1, d2), dev)
     _launch(dev, where, L.w8a8_moe_experts, X.data_ptr(), ids.data_ptr(), R, E, w1.q_w.data_ptr(), w1.s_w.data_ptr(),

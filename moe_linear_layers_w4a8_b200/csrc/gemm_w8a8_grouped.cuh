@@ -59,6 +59,7 @@ struct W8GroupedParams {
     uint16_t* Y;
     int ldy;
     int vec16;                   // Y and ldy allow 16-byte row stores
+    int early;                   // offsets are final before the preceding kernel is complete
     int split_tiles;             // tiles below which units may be split (0: never)
     int32_t* partial;            // [2 * grid][2][BN][128] int32 partial tiles
     unsigned long long* counts;  // [split_tiles] arrivals of this launch
@@ -275,8 +276,9 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
         tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();
     }
-    // offsets and rows may come from the kernel launched just before
-    pdl_wait_prerequisites();
+    // The rows, and the offsets too unless `early`, may come from the kernel
+    // launched just before; the weights do not, and stream meanwhile.
+    if (!p.early) pdl_wait_prerequisites();
     build_group_table(g, p.offsets, p.E, p.R, BN, blockIdx.x == 0 ? p.status : nullptr);
     tc_fence_before();
     __syncthreads();
@@ -291,6 +293,7 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
         // ------------------------------------------------------ producers --
         if (lane == 0) {
             const bool is_w = warp == 0;
+            if (!is_w) pdl_wait_prerequisites();
             uint64_t* full = is_w ? w_full : x_full;
             Ring rs;
             long long issued = 0;
@@ -386,6 +389,7 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
         constexpr int LB = GATEUP ? (BN < 64 ? BN / 2 : 32) : (BN < 32 ? BN : 32);
         constexpr int STEP = GATEUP ? 2 * LB : LB;
         const int et = threadIdx.x - kW8GEpiWarp0 * 32;  // 0..255
+        pdl_wait_prerequisites();
         Ring ra;
         while (walk.next(tile, kb0, kb1)) {
             const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);

@@ -102,8 +102,11 @@ __global__ void __launch_bounds__(kQuantThreads) quant_act_kernel(
     // Launched the same way itself, this kernel may start while the preceding
     // kernel is still running: X and the outputs are touched only after that
     // kernel completed.
-    pdl_launch_dependents();
+    // The next kernel may start once this one knows the preceding kernel to be
+    // complete: what earlier kernels of the stream wrote (expert offsets) is
+    // then final for it too.
     pdl_wait_prerequisites();
+    pdl_launch_dependents();
     const int m = blockIdx.x;
     if (!used.has(m)) return;
     const int tid = threadIdx.x;
@@ -180,8 +183,8 @@ __global__ void __launch_bounds__(kQuantThreads) quant_act_kernel(
 __global__ void __launch_bounds__(kQuantThreads) quant_act_long_kernel(
     const uint16_t* __restrict__ X, int K, int ldx, int8_t* __restrict__ q, float* __restrict__ s_x,
     int32_t* __restrict__ rowsum, int group, const RowRange used, int32_t* status) {
-    pdl_launch_dependents();
     pdl_wait_prerequisites();
+    pdl_launch_dependents();
     const int m = blockIdx.x;
     if (!used.has(m)) return;
     const int tid = threadIdx.x;
@@ -242,8 +245,8 @@ __global__ void __launch_bounds__(32 * kQuantRowsPerCta) quant_act_rows_kernel(
     const uint16_t* __restrict__ X, int rows, int K, int ldx, int8_t* __restrict__ q, float* __restrict__ s_x,
     int32_t* __restrict__ rowsum, int group, const int32_t* __restrict__ dest, int dest_k, const RowRange used,
     int32_t* status) {
-    pdl_launch_dependents();
     pdl_wait_prerequisites();
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int m = blockIdx.x * kQuantRowsPerCta + (threadIdx.x >> 5);
     if (m >= rows || !used.has(m)) return;  // warp-uniform
@@ -386,12 +389,9 @@ __global__ void __launch_bounds__(128) pack_weights_kernel(const float* __restri
 // experts l, l+32, ...; the exp-sum uses a fixed reduction tree.
 // ---------------------------------------------------------------------------
 template <int EPL>
-__global__ void __launch_bounds__(256) route_topk_kernel(const float* __restrict__ logits, int T, int E,
-                                                         int topk, int32_t* __restrict__ idx,
-                                                         float* __restrict__ p, int32_t* status) {
-    const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+__device__ __forceinline__ void route_token(const float* __restrict__ logits, int t, int E, int topk,
+                                            int32_t* __restrict__ idx, float* __restrict__ p, int32_t* status) {
     const int lane = threadIdx.x & 31;
-    if (t >= T) return;
     const float* l = logits + (size_t)t * E;
     float v[EPL];
     bool bad = false;
@@ -442,6 +442,15 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const float* __restrict
         }
     }
     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) report_status(status, kStatusNonfinite);
+}
+
+template <int EPL>
+__global__ void __launch_bounds__(256) route_topk_kernel(const float* __restrict__ logits, int T, int E,
+                                                         int topk, int32_t* __restrict__ idx,
+                                                         float* __restrict__ p, int32_t* status) {
+    const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    if (t >= T) return;
+    route_token<EPL>(logits, t, E, topk, idx, p, status);
 }
 
 // ---------------------------------------------------------------------------
@@ -513,6 +522,61 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const int32_
         __syncthreads();
         for (int e = tid; e < E; e += kDispatchThreads) base[e] += cnt[e];
         __syncthreads();
+    }
+}
+
+// Routing and dispatch of a few tokens (T <= 16) in one CTA: a layer step of
+// single tokens is a chain of launches whose own work is short (routing and
+// dispatch as two launches: 4.0 + 5.8 us for one token of 64 experts, most of
+// it launch and the walk over the experts by one thread; this kernel: 5.0 us).
+// Each warp routes a token; a pair's rank among its expert's is counted over
+// the earlier pairs; the offsets are one warp's scan.  Same outputs as
+// route_topk_kernel and dispatch_kernel.
+constexpr int kRouteDispatchTokens = 16;
+
+template <int EPL>
+__global__ void __launch_bounds__(32 * kRouteDispatchTokens) route_dispatch_kernel(
+    const float* __restrict__ logits, int T, int E, int topk, int32_t* __restrict__ idx, float* __restrict__ p,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ inv, int32_t* status) {
+    __shared__ int32_t first[kMaxExperts];                         // counts, then first positions
+    __shared__ int32_t expert[kRouteDispatchTokens * 16];          // of every pair
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int e = tid; e < E; e += blockDim.x) first[e] = 0;
+    if (warp < T) route_token<EPL>(logits, warp, E, topk, idx, p, status);
+    __syncthreads();
+    const int pairs = T * topk;                                    // at most 256
+    int e = 0;
+    if (tid < pairs) {
+        e = idx[tid];
+        expert[tid] = e;
+        atomicAdd(&first[e], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {  // exclusive scan, one run of consecutive experts per lane
+        const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
+        int32_t sum = 0;
+        for (int k = e0; k < e1; ++k) sum += first[k];
+        int32_t inc = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+            if (lane >= off) inc += v;
+        }
+        int32_t run = inc - sum;
+        for (int k = e0; k < e1; ++k) {
+            const int32_t c = first[k];
+            first[k] = run;
+            offsets[k] = run;
+            run += c;
+        }
+        if (lane == 31) offsets[E] = pairs;
+    }
+    __syncthreads();
+    if (tid < pairs) {
+        int32_t pos = first[e];
+        for (int k = 0; k < tid; ++k) pos += expert[k] == e;
+        inv[tid] = pos;
+        perm[pos] = tid;
     }
 }
 
@@ -630,6 +694,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
                                                       const float* __restrict__ p,
                                                       const int32_t* __restrict__ inv, int T, int topk, int H,
                                                       uint16_t* __restrict__ out) {
+    pdl_wait_prerequisites();
     const int cpr = H >> 3;
     const long long gid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (gid >= (long long)T * cpr) return;
@@ -637,6 +702,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+#pragma unroll 4
     for (int j = 0; j < topk; ++j) {
         // inv == null: the rows are already in (token, slot) order
         const int r = inv ? __ldg(inv + (size_t)t * topk + j) : t * topk + j;

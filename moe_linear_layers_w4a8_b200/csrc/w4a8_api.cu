@@ -353,6 +353,20 @@ w4a8_status launch_route(const float* logits, int T, int E, int topk, int32_t* i
     return last_cuda();
 }
 
+// Routing and dispatch of T <= kRouteDispatchTokens tokens in one launch.
+w4a8_status launch_route_dispatch(const float* logits, int T, int E, int topk, int32_t* idx, float* w,
+                                  int32_t* offsets, int32_t* perm, int32_t* inv, int32_t* status, cudaStream_t s) {
+    switch ((E + 31) / 32) {
+#define W4A8_ROUTE(n) case n: route_dispatch_kernel<n><<<1, 32 * kRouteDispatchTokens, 0, s>>>(logits, T, E, topk, idx, w, offsets, perm, inv, status); break;
+        W4A8_ROUTE(1) W4A8_ROUTE(2) W4A8_ROUTE(3) W4A8_ROUTE(4) W4A8_ROUTE(5) W4A8_ROUTE(6) W4A8_ROUTE(7)
+        W4A8_ROUTE(8) W4A8_ROUTE(9) W4A8_ROUTE(10) W4A8_ROUTE(11) W4A8_ROUTE(12) W4A8_ROUTE(13)
+        W4A8_ROUTE(14) W4A8_ROUTE(15) W4A8_ROUTE(16)
+#undef W4A8_ROUTE
+        default: return W4A8_ERR_UNSUPPORTED_SHAPE;
+    }
+    return last_cuda();
+}
+
 // Expert offsets, m-tile prefix for tiles of bn rows, and the permutation of
 // T * topk pairs, all ids already in [0, E).  dcnt: dispatch_ctas(T) * E ints.
 w4a8_status launch_dispatch(const int32_t* idx, int T, int E, int topk, int bn, int32_t* offsets, int32_t* mtile_off,
@@ -549,9 +563,12 @@ bool make_w8_grouped_tmap(CUtensorMap* map, const void* base, int E, int N, int 
 }
 
 // The grouped product (gate_up: with silu(gate) * up).  N: output columns.
+// early: the offsets were written before the preceding kernel of the stream
+// let this one start (a quantization kernel does so once all before it is
+// complete).
 w4a8_status launch_w8_grouped(const int8_t* qx, const float* s_x, const int32_t* offsets, int R, int E,
                               const int8_t* q_w, const float* s_w, int N, int K, bool gate_up, uint16_t* Y, int ldy,
-                              void* workspace, int32_t* dev_status, cudaStream_t s) {
+                              void* workspace, int32_t* dev_status, cudaStream_t s, bool early) {
     const W8GroupedPlan pl = plan_w8_grouped(R, E, N, K, gate_up, sm_count_current());
     CUtensorMap tw, tx;
     if (!make_w8_grouped_tmap(&tw, q_w, E, N, K, gate_up) ||
@@ -570,6 +587,7 @@ w4a8_status launch_w8_grouped(const int8_t* qx, const float* s_x, const int32_t*
     p.Y = Y;
     p.ldy = ldy;
     p.vec16 = (aligned16(Y) && ldy % 8 == 0) ? 1 : 0;
+    p.early = early ? 1 : 0;
     p.split_tiles = pl.split_tiles;
     if (pl.split_tiles > 0) {
         p.partial = static_cast<int32_t*>(workspace);
@@ -1296,7 +1314,7 @@ w4a8_status w8a8_grouped_gemm(const int8_t* qx, const float* s_x, const int32_t*
     const size_t need = w8a8_grouped_workspace_size(R, E, w);
     if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return W4A8_ERR_WORKSPACE;
     return launch_w8_grouped(qx, s_x, offsets, R, E, q_w, s_w, w->N, w->K, false, Y, ldy, workspace, dev_status,
-                             static_cast<cudaStream_t>(stream));
+                             static_cast<cudaStream_t>(stream), false);
 }
 
 size_t w8a8_grouped_linear_workspace_size(int R, int E, const w4a8_wdesc* w) {
@@ -1325,7 +1343,7 @@ w4a8_status w8a8_grouped_linear(const uint16_t* X, int R, int ldx, const int32_t
     st = launch_quant(X, R, w->K, ldx, qx, sx, nullptr, 0, nullptr, 0, dev_status, s, false,
                       RowRange{offsets, offsets + E});
     if (st != W4A8_OK) return st;
-    return launch_w8_grouped(qx, sx, offsets, R, E, q_w, s_w, w->N, w->K, false, Y, ldy, ws + go, dev_status, s);
+    return launch_w8_grouped(qx, sx, offsets, R, E, q_w, s_w, w->N, w->K, false, Y, ldy, ws + go, dev_status, s, true);
 }
 
 }  // extern "C"
@@ -1348,26 +1366,33 @@ w4a8_status moe_w8_impl(const uint16_t* X, const float* logits, const int32_t* p
     float* sh = reinterpret_cast<float*>(ws + L.base.sh);
     uint16_t* yd = reinterpret_cast<uint16_t*>(ws + L.base.yd);
     w4a8_status st;
-    if (pre_ids) {
-        preroute_kernel<<<(unsigned)((T + 255) / 256), 256, 0, s>>>(pre_ids, T, E, idx, wts, dev_status);
-        st = last_cuda();
+    int32_t* perm = reinterpret_cast<int32_t*>(ws + L.base.perm);
+    if (!pre_ids && T <= kRouteDispatchTokens) {
+        if ((st = launch_route_dispatch(logits, T, E, topk, idx, wts, offsets, perm, inv, dev_status, s)) != W4A8_OK)
+            return st;
     } else {
-        st = launch_route(logits, T, E, topk, idx, wts, dev_status, s);
+        if (pre_ids) {
+            preroute_kernel<<<(unsigned)((T + 255) / 256), 256, 0, s>>>(pre_ids, T, E, idx, wts, dev_status);
+            st = last_cuda();
+        } else {
+            st = launch_route(logits, T, E, topk, idx, wts, dev_status, s);
+        }
+        if (st != W4A8_OK) return st;
+        st = launch_dispatch(idx, T, E, topk, 128, offsets, reinterpret_cast<int32_t*>(ws + L.base.mtile_off), perm, inv,
+                             reinterpret_cast<int32_t*>(ws + L.base.dcnt), s);
+        if (st != W4A8_OK) return st;
     }
+    // From here every kernel waits for the one before it inside (programmatic
+    // stream serialization), so that a launch's start-up overlaps that one's end.
+    if ((st = launch_quant(X, T, H, H, qx, sx, nullptr, 0, inv, topk, dev_status, s, true)) != W4A8_OK) return st;
+    st = launch_w8_grouped(qx, sx, offsets, R, E, w1_q, w1_s, I, H, true, h, I, ws + L.split, dev_status, s, true);
     if (st != W4A8_OK) return st;
-    st = launch_dispatch(idx, T, E, topk, 128, offsets, reinterpret_cast<int32_t*>(ws + L.base.mtile_off),
-                         reinterpret_cast<int32_t*>(ws + L.base.perm), inv,
-                         reinterpret_cast<int32_t*>(ws + L.base.dcnt), s);
-    if (st != W4A8_OK) return st;
-    if ((st = launch_quant(X, T, H, H, qx, sx, nullptr, 0, inv, topk, dev_status, s)) != W4A8_OK) return st;
-    st = launch_w8_grouped(qx, sx, offsets, R, E, w1_q, w1_s, I, H, true, h, I, ws + L.split, dev_status, s);
-    if (st != W4A8_OK) return st;
-    if ((st = launch_quant(h, R, I, I, qh, sh, nullptr, 0, nullptr, 0, dev_status, s)) != W4A8_OK) return st;
-    st = launch_w8_grouped(qh, sh, offsets, R, E, w2_q, w2_s, H, I, false, yd, H, ws + L.split, dev_status, s);
+    if ((st = launch_quant(h, R, I, I, qh, sh, nullptr, 0, nullptr, 0, dev_status, s, true)) != W4A8_OK) return st;
+    st = launch_w8_grouped(qh, sh, offsets, R, E, w2_q, w2_s, H, I, false, yd, H, ws + L.split, dev_status, s, true);
     if (st != W4A8_OK) return st;
     const long long n = (long long)T * (H / 8);
-    combine_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(yd, wts, inv, T, topk, H, out);
-    return last_cuda();
+    st = launch_maybe_pdl(combine_kernel, (unsigned)((n + 255) / 256), 256, s, true, yd, wts, inv, T, topk, H, out);
+    return st != W4A8_OK ? st : last_cuda();
 }
 
 }  // namespace
