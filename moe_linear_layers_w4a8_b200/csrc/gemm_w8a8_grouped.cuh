@@ -34,10 +34,11 @@
 //     count adds all parts and writes the output.  Integer sums are exact in
 //     any order, so results do not depend on who comes last, and no CTA ever
 //     waits for another.
-//   * Warp 0 streams weights, warp 10 rows, one lane of warp 1 issues the
-//     MMAs, warps 2-9 drain (each its own 32 columns, staged in 2 KB of shared
-//     memory of its own and written as 16-byte pieces).  Two accumulator
-//     pairs alternate, so a drain overlaps the next tile's MMAs.
+//   * Warp 0 streams weights, the last warp rows, one lane of warp 1 issues the
+//     MMAs, 16 warps drain (32 columns each, staged in shared memory of its
+//     own and written as 16-byte pieces; with 8 warps the drain took 8,400 of a
+//     tile's 11,000 cycles at K = 1408).  Two accumulator pairs alternate, so a
+//     drain overlaps the next tile's MMAs.
 #pragma once
 
 #include <cstdint>
@@ -68,9 +69,10 @@ struct W8GroupedParams {
     unsigned long long wait_ns;
 };
 
-constexpr int kW8GThreads = 352;     // 2 producers, MMA, 8 epilogue warps
+constexpr int kW8GEpiWarps = 16;     // four groups, each with every quarter of the 128 columns
+constexpr int kW8GThreads = 32 * (kW8GEpiWarps + 3);   // and 2 producers, MMA
 constexpr int kW8GEpiWarp0 = 2;
-constexpr int kW8GXWarp = 10;
+constexpr int kW8GXWarp = kW8GEpiWarp0 + kW8GEpiWarps;
 constexpr int kGroupedMaxExperts = 512;
 
 template <int BN>
@@ -79,7 +81,8 @@ struct W8GCfg {
     static constexpr int XBOX = BN < 64 ? BN : 64;          // rows per activation request
     static constexpr int B_STAGE = BN * 128;
     static constexpr int STAGE = A_STAGE + B_STAGE;
-    static constexpr int STG = 8 * 2048;                    // output staging: 32 tokens x 32 columns per warp
+    static constexpr int LB = BN < 32 ? 8 : 16;             // tokens per epilogue batch
+    static constexpr int STG = kW8GEpiWarps * 1024;         // output staging: 16 tokens x 32 columns per warp
     static constexpr int TABLE = 3 * (kGroupedMaxExperts + 1) * 4;
     static constexpr int NST_RAW = (227 * 1024 - 1024 - STG - TABLE - 512) / STAGE;
     static constexpr int NST = NST_RAW > 8 ? 8 : NST_RAW;
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
     uint64_t* x_full = w_full + C::NST;     // [NST] rows landed
     uint64_t* empty = x_full + C::NST;      // [NST] their MMAs completed
     uint64_t* acc_full = empty + C::NST;    // [2] accumulator pair's MMAs completed
-    uint64_t* acc_empty = acc_full + 2;     // [2] drained by the 8 epilogue warps
+    uint64_t* acc_empty = acc_full + 2;     // [2] drained by the epilogue warps
     uint64_t* drain = acc_empty + 2;        // [1] every MMA of the CTA completed
     GroupTable g;
     g.beg = reinterpret_cast<int32_t*>(smem + C::OFF_TABLE);
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 8);
+            mbar_init(&acc_empty[i], kW8GEpiWarps);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -335,8 +338,12 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
         // uniform over the warp, an MMA's descriptors sit in uniform registers
         // instead of being moved there one by one (measured in the W4A16
         // kernel: 135 -> 32 cycles for each MMA).
+        // A wait costs its latency even when the stage is there, and the MMA
+        // queue holds little more than a stage: so the next stage is asked for
+        // before this one's MMAs are issued.
         const bool leader = elect_one();
         Ring rs, ra;
+        bool there = false;   // the stage's copies were seen to have landed
         bool ok = true;
         while (ok && walk.next(tile, kb0, kb1)) {
             const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
@@ -347,11 +354,18 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
             tc_fence_after();
             const uint32_t d0 = tmem_base + ra.idx * (2 * BN);
             for (int kb = kb0; kb < kb1; ++kb) {
-                ok = warp_wait_bounded(&w_full[rs.idx], rs.phase, wc) && warp_wait_bounded(&x_full[rs.idx], rs.phase, wc);
-                if (!ok) break;
+                if (!there) {
+                    ok = warp_wait_bounded(&w_full[rs.idx], rs.phase, wc) &&
+                         warp_wait_bounded(&x_full[rs.idx], rs.phase, wc);
+                    if (!ok) break;
+                }
                 tc_fence_after();
+                const uint32_t a_addr = smem_u32(smem + rs.idx * C::STAGE);
+                uint64_t* const done = &empty[rs.idx];
+                rs.next(C::NST);
+                const bool next_w = mbar_test_wait(&w_full[rs.idx], rs.phase);
+                const bool next_x = mbar_test_wait(&x_full[rs.idx], rs.phase);
                 if (leader) {
-                    const uint32_t a_addr = smem_u32(smem + rs.idx * C::STAGE);
                     const uint64_t adesc = umma_desc_kmajor(a_addr, 128);
                     const uint64_t bdesc = umma_desc_kmajor(a_addr + C::A_STAGE, 128);
 #pragma unroll
@@ -360,10 +374,9 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
                         mma_i8(d0, adesc + 2 * kk, bdesc + 2 * kk, idesc, acc);
                         if (two) mma_i8(d0 + BN, adesc + (128 * 128 >> 4) + 2 * kk, bdesc + 2 * kk, idesc, acc);
                     }
-                    tc_commit(&empty[rs.idx]);
+                    tc_commit(done);
                 }
-                __syncwarp();
-                rs.next(C::NST);
+                there = __all_sync(0xFFFFFFFFu, next_w && next_x) != 0;
             }
             if (!ok) break;
             if (leader) tc_commit(&acc_full[ra.idx]);
@@ -382,26 +395,26 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
     } else {
         // ------------------------------------------------------- epilogue --
         const int q = warp & 3;                          // TMEM lane quadrant
-        const int grp = (warp - kW8GEpiWarp0) >> 2;      // plain: column half; gate_up: every other token batch
+        const int grp = (warp - kW8GEpiWarp0) >> 2;      // plain: column half and every other batch; gate_up: every 4th
         const uint32_t lane_addr = ((uint32_t)(q * 32)) << 16;
-        uint16_t* stg = reinterpret_cast<uint16_t*>(smem + C::OFF_STG) + (warp - kW8GEpiWarp0) * 1024;
-        // tokens per batch: a thread holds LB accumulators (gate_up: LB pairs)
-        constexpr int LB = GATEUP ? (BN < 64 ? BN / 2 : 32) : (BN < 32 ? BN : 32);
-        constexpr int STEP = GATEUP ? 2 * LB : LB;
-        const int et = threadIdx.x - kW8GEpiWarp0 * 32;  // 0..255
+        uint16_t* stg = reinterpret_cast<uint16_t*>(smem + C::OFF_STG) + (warp - kW8GEpiWarp0) * 512;
+        constexpr int LB = C::LB;                        // a thread holds LB accumulators (gate_up: LB pairs)
+        constexpr int STEP = GATEUP ? 4 * LB : 2 * LB;
+        constexpr int kEpiThreads = 32 * kW8GEpiWarps;
+        const int et = threadIdx.x - kW8GEpiWarp0 * 32;
         pdl_wait_prerequisites();
         Ring ra;
         while (walk.next(tile, kb0, kb1)) {
             const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
             bool ok = warp_wait_bounded(&acc_full[ra.idx], ra.phase, wc);
-            if (walk.split) ok = !named_bar_or(1, 256, !ok);  // one decision before the barriers below
+            if (walk.split) ok = !named_bar_or(1, kEpiThreads, !ok);  // one decision before the barriers below
             if (!ok) break;
             tc_fence_after();
             const uint32_t tacc = tmem_base + lane_addr + ra.idx * (2 * BN);
-            const int half = GATEUP ? 0 : grp;
+            const int half = GATEUP ? 0 : grp & 1;
             const int c_in = q * 32 + lane;                                      // column within the 128
             const int col0 = GATEUP ? gt.nt * 128 + q * 32 : gt.nt * 256 + half * 128 + q * 32;  // the warp's first
-            const int first = GATEUP ? grp * LB : 0;                             // the warp's first token batch
+            const int first = GATEUP ? grp * LB : (grp >> 1) * LB;               // the warp's first token batch
             const bool live = col0 < p.N;                                        // warp-uniform
             const int32_t* parts = nullptr;   // the tile's partial tiles, when this CTA adds them
             int nparts = 0, c_first = 0;
@@ -429,13 +442,13 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
                 const int t0 = (int)tile * p.KB;
                 c_first = t0 / walk.Q;
                 nparts = (t0 + p.KB - 1) / walk.Q - c_first + 1;
-                named_bar_sync(1, 256);
+                named_bar_sync(1, kEpiThreads);
                 if (et == 0) {
                     __threadfence();
                     *last_flag = count_in(p.counts + tile, p.epoch, nparts) == nparts - 1;
                     __threadfence();
                 }
-                named_bar_sync(1, 256);
+                named_bar_sync(1, kEpiThreads);
                 write = live && *reinterpret_cast<volatile int*>(last_flag) != 0;
                 // the CTA holding the tile's first k-blocks stored to its slot 1, the others to slot 0
                 parts = p.partial;
@@ -477,7 +490,10 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
                         float y = sx * (sw0 * (float)(int32_t)a[j]);
                         if constexpr (GATEUP) {
                             const float up = sx * (sw1 * (float)(int32_t)b[j]);
-                            y = (y / (1.0f + expf(-y))) * up;
+                            // the bf16 rounding of h is 2^-9: __expf and the fast quotient are within 2^-20
+                            // for |y| < 88 and give 0 below; with the exact ones this epilogue, not the
+                            // MMAs, set the pace (13,000 of 15,000 cycles a tile at K = 2048)
+                            y = __fdividef(y, 1.0f + __expf(-y)) * up;
                         }
                         stg[j * 32 + lane] = f32_to_bf16_bits(y);
                     }

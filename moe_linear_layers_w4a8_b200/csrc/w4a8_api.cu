@@ -1340,7 +1340,7 @@ w4a8_status w8a8_grouped_linear(const uint16_t* X, int R, int ldx, const int32_t
     int8_t* qx = reinterpret_cast<int8_t*>(ws);
     float* sx = reinterpret_cast<float*>(ws + sxo);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = launch_quant(X, R, w->K, ldx, qx, sx, nullptr, 0, nullptr, 0, dev_status, s, false,
+    st = launch_quant(X, R, w->K, ldx, qx, sx, nullptr, 0, nullptr, 0, dev_status, s, true,
                       RowRange{offsets, offsets + E});
     if (st != W4A8_OK) return st;
     return launch_w8_grouped(qx, sx, offsets, R, E, q_w, s_w, w->N, w->K, false, Y, ldy, ws + go, dev_status, s, true);
