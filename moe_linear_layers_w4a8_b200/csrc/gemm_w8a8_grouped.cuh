@@ -34,8 +34,8 @@
 //     count adds all parts and writes the output.  Integer sums are exact in
 //     any order, so results do not depend on who comes last, and no CTA ever
 //     waits for another.
-//   * Warp 0 streams weights, the last warp rows, one lane of warp 1 issues the
-//     MMAs, 16 warps drain (32 columns each, staged in shared memory of its
+//   * One warp streams weights, one rows, two issue the MMAs (one accumulator
+//     each), 16 warps drain (32 columns each, staged in shared memory of its
 //     own and written as 16-byte pieces; with 8 warps the drain took 8,400 of a
 //     tile's 11,000 cycles at K = 1408).  Two accumulator pairs alternate, so a
 //     drain overlaps the next tile's MMAs.
@@ -70,9 +70,10 @@ struct W8GroupedParams {
 };
 
 constexpr int kW8GEpiWarps = 16;     // four groups, each with every quarter of the 128 columns
-constexpr int kW8GThreads = 32 * (kW8GEpiWarps + 3);   // and 2 producers, MMA
+constexpr int kW8GThreads = 32 * (kW8GEpiWarps + 4);   // and 2 producers, 2 MMA warps
 constexpr int kW8GEpiWarp0 = 2;
 constexpr int kW8GXWarp = kW8GEpiWarp0 + kW8GEpiWarps;
+constexpr int kW8GMma2Warp = kW8GXWarp + 1;
 constexpr int kGroupedMaxExperts = 512;
 
 template <int BN>
@@ -88,7 +89,7 @@ struct W8GCfg {
     static constexpr int NST = NST_RAW > 8 ? 8 : NST_RAW;
     static constexpr int OFF_STG = NST * STAGE;
     static constexpr int OFF_BAR = OFF_STG + STG;
-    static constexpr int NUM_BARS = 3 * NST + 5;
+    static constexpr int NUM_BARS = 3 * NST + 6;
     static constexpr int OFF_TABLE = OFF_BAR + NUM_BARS * 8;
     static constexpr int OFF_MISC = OFF_TABLE + TABLE;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
     uint64_t* empty = x_full + C::NST;      // [NST] their MMAs completed
     uint64_t* acc_full = empty + C::NST;    // [2] accumulator pair's MMAs completed
     uint64_t* acc_empty = acc_full + 2;     // [2] drained by the epilogue warps
-    uint64_t* drain = acc_empty + 2;        // [1] every MMA of the CTA completed
+    uint64_t* drain = acc_empty + 2;        // [2] every MMA of a warp completed
     GroupTable g;
     g.beg = reinterpret_cast<int32_t*>(smem + C::OFF_TABLE);
     g.cnt = g.beg + kGroupedMaxExperts + 1;
@@ -262,13 +263,14 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
         for (int i = 0; i < C::NST; ++i) {
             mbar_init(&w_full[i], 1);
             mbar_init(&x_full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_full[i], 2);
             mbar_init(&acc_empty[i], kW8GEpiWarps);
         }
-        mbar_init(drain, 1);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         *abort_flag = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -332,8 +334,10 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
                 (void)wait_bounded(&full[d.idx], d.phase, wd);
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == kW8GMma2Warp) {
         // ------------------------------------------------------ MMA issue --
+        // One warp for each of the pair's accumulators: what a warp spends between
+        // two stages (commit, wait) is covered by the other's MMAs.
         // The whole warp runs the loop and one lane issues: with every value
         // uniform over the warp, an MMA's descriptors sit in uniform registers
         // instead of being moved there one by one (measured in the W4A16
@@ -341,6 +345,7 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
         // A wait costs its latency even when the stage is there, and the MMA
         // queue holds little more than a stage: so the next stage is asked for
         // before this one's MMAs are issued.
+        const int half = warp == 1 ? 0 : 1;
         const bool leader = elect_one();
         Ring rs, ra;
         bool there = false;   // the stage's copies were seen to have landed
@@ -348,11 +353,11 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
         while (ok && walk.next(tile, kb0, kb1)) {
             const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
             const uint32_t idesc = idesc_i8((gt.rows + 15) & ~15);
-            const bool two = GATEUP || p.N - gt.nt * 256 > 128;
+            const bool mine = half == 0 || GATEUP || p.N - gt.nt * 256 > 128;   // some of the box's columns exist
             ok = warp_wait_bounded(&acc_empty[ra.idx], ra.phase ^ 1u, wc);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t d0 = tmem_base + ra.idx * (2 * BN);
+            const uint32_t d = tmem_base + ra.idx * (2 * BN) + half * BN;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!there) {
                     ok = warp_wait_bounded(&w_full[rs.idx], rs.phase, wc) &&
@@ -366,13 +371,12 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
                 const bool next_w = mbar_test_wait(&w_full[rs.idx], rs.phase);
                 const bool next_x = mbar_test_wait(&x_full[rs.idx], rs.phase);
                 if (leader) {
-                    const uint64_t adesc = umma_desc_kmajor(a_addr, 128);
+                    const uint64_t adesc = umma_desc_kmajor(a_addr + half * (128 * 128), 128);
                     const uint64_t bdesc = umma_desc_kmajor(a_addr + C::A_STAGE, 128);
+                    if (mine) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t acc = (kb > kb0 || kk > 0) ? 1u : 0u;
-                        mma_i8(d0, adesc + 2 * kk, bdesc + 2 * kk, idesc, acc);
-                        if (two) mma_i8(d0 + BN, adesc + (128 * 128 >> 4) + 2 * kk, bdesc + 2 * kk, idesc, acc);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_i8(d, adesc + 2 * kk, bdesc + 2 * kk, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
                     }
                     tc_commit(done);
                 }
@@ -385,11 +389,11 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
         }
         // drain: every MMA issued above completes before TMEM is freed
         if (leader) {
-            tc_commit(drain);
+            tc_commit(&drain[half]);
             WaitCtx wd = wc;
             volatile int no_abort = 0;
             wd.abort = &no_abort;
-            (void)wait_bounded(drain, 0, wd);
+            (void)wait_bounded(&drain[half], 0, wd);
         }
         __syncwarp();
     } else {
