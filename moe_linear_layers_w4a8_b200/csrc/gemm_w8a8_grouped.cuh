@@ -53,7 +53,8 @@ struct W8GroupedParams {
     int N;                       // output columns (gate_up: I)
     int K, KB;                   // KB = K / 128 k-blocks
     int E, R;
-    int n_tiles;                 // ceil(N / 256), gate_up: ceil(I / 128)
+    int halves;                  // boxes of 128 columns to a tile: 2, plain and few tiles: 1
+    int n_tiles;                 // ceil(N / (128 halves)), gate_up: ceil(I / 128)
     const int32_t* offsets;      // [E + 1] device
     const float* s_w;            // [E][N], gate_up: [E][2I]
     const float* s_x;            // [R]
@@ -306,12 +307,12 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
             while (ok && walk.next(tile, kb0, kb1)) {
                 const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
                 const int boxes = gt.rows > C::XBOX ? 2 : 1;
-                const int col = gt.nt * (GATEUP ? 128 : 256);
+                const int col = gt.nt * (GATEUP ? 128 : 128 * p.halves);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait_bounded(&empty[rs.idx], rs.phase ^ 1u, wc)) { ok = false; break; }
                     uint8_t* st = smem + rs.idx * C::STAGE;
                     if (is_w) {
-                        mbar_arrive_expect_tx(&full[rs.idx], C::A_STAGE);
+                        mbar_arrive_expect_tx(&full[rs.idx], p.halves * (C::A_STAGE / 2));
                         tma_load_4d(st, &tmap_w, &full[rs.idx], kb * 128, col, 0, gt.e);
                     } else {
                         mbar_arrive_expect_tx(&full[rs.idx], boxes * (C::XBOX * 128));
@@ -353,7 +354,8 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
         while (ok && walk.next(tile, kb0, kb1)) {
             const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
             const uint32_t idesc = idesc_i8((gt.rows + 15) & ~15);
-            const bool mine = half == 0 || GATEUP || p.N - gt.nt * 256 > 128;   // some of the box's columns exist
+            // some of the box's columns exist
+            const bool mine = half == 0 || GATEUP || (p.halves == 2 && p.N - gt.nt * 256 > 128);
             ok = warp_wait_bounded(&acc_empty[ra.idx], ra.phase ^ 1u, wc);
             if (!ok) break;
             tc_fence_after();
@@ -417,9 +419,10 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
             const uint32_t tacc = tmem_base + lane_addr + ra.idx * (2 * BN);
             const int half = GATEUP ? 0 : grp & 1;
             const int c_in = q * 32 + lane;                                      // column within the 128
-            const int col0 = GATEUP ? gt.nt * 128 + q * 32 : gt.nt * 256 + half * 128 + q * 32;  // the warp's first
+            // the warp's first column
+            const int col0 = GATEUP ? gt.nt * 128 + q * 32 : (gt.nt * p.halves + half) * 128 + q * 32;
             const int first = GATEUP ? grp * LB : (grp >> 1) * LB;               // the warp's first token batch
-            const bool live = col0 < p.N;                                        // warp-uniform
+            const bool live = half < p.halves && col0 < p.N;                     // warp-uniform
             const int32_t* parts = nullptr;   // the tile's partial tiles, when this CTA adds them
             int nparts = 0, c_first = 0;
             bool write = live;

@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const float* __restrict
                                                          int topk, int32_t* __restrict__ idx,
                                                          float* __restrict__ p, int32_t* status) {
     const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    pdl_launch_dependents();
     if (t >= T) return;
     route_token<EPL>(logits, t, E, topk, idx, p, status);
 }
@@ -476,22 +477,42 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const int32_
     __shared__ uint32_t bits[kDispatchThreads / 32][kMaxExperts];
     __shared__ int32_t wpre[kDispatchThreads / 32][kMaxExperts];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
     for (int e = tid; e < E; e += kDispatchThreads) cnt[e] = 0;
     __syncthreads();
     const int pairs = T * topk;
     for (int i = tid; i < pairs; i += kDispatchThreads) atomicAdd(&cnt[idx[i]], 1);
     __syncthreads();
-    if (tid == 0) {
-        int32_t run = 0, tiles = 0;
-        for (int e = 0; e < E; ++e) {
-            offsets[e] = run;
-            mtile_off[e] = tiles;
-            base[e] = run;
-            run += cnt[e];
+    if (warp == 0) {  // exclusive scans, one run of consecutive experts per lane
+        const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
+        int32_t rows = 0, tiles = 0;
+        for (int e = e0; e < e1; ++e) {
+            rows += cnt[e];
             tiles += (cnt[e] + bn - 1) / bn;
         }
-        offsets[E] = run;
-        mtile_off[E] = tiles;
+        int32_t run = rows, trun = tiles;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int32_t a = __shfl_up_sync(0xFFFFFFFFu, run, off), b = __shfl_up_sync(0xFFFFFFFFu, trun, off);
+            if (lane >= off) {
+                run += a;
+                trun += b;
+            }
+        }
+        if (lane == 31) {
+            offsets[E] = run;
+            mtile_off[E] = trun;
+        }
+        run -= rows;
+        trun -= tiles;
+        for (int e = e0; e < e1; ++e) {
+            offsets[e] = run;
+            mtile_off[e] = trun;
+            base[e] = run;
+            run += cnt[e];
+            trun += (cnt[e] + bn - 1) / bn;
+        }
     }
     __syncthreads();
     for (int t0 = 0; t0 < T; t0 += kDispatchThreads) {
@@ -541,6 +562,7 @@ __global__ void __launch_bounds__(32 * kRouteDispatchTokens) route_dispatch_kern
     __shared__ int32_t first[kMaxExperts];                         // counts, then first positions
     __shared__ int32_t expert[kRouteDispatchTokens * 16];          // of every pair
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
     for (int e = tid; e < E; e += blockDim.x) first[e] = 0;
     if (warp < T) route_token<EPL>(logits, warp, E, topk, idx, p, status);
     __syncthreads();
@@ -592,6 +614,8 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_count_kernel(const 
                                                                           int32_t* __restrict__ cnt_g) {
     __shared__ int32_t cnt[kMaxExperts];
     const int c = blockIdx.x, tid = threadIdx.x;
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
     for (int e = tid; e < E; e += kDispatchThreads) cnt[e] = 0;
     __syncthreads();
     const long long p0 = (long long)c * tpc * topk;
@@ -609,6 +633,8 @@ __global__ void __launch_bounds__(kDispatchScanThreads) dispatch_scan_kernel(int
                                                                             int32_t* __restrict__ mtile_off) {
     __shared__ int32_t tot[kMaxExperts], til[kMaxExperts];
     const int e = threadIdx.x;
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
     int32_t total = 0;
     if (e < E)
         for (int c = 0; c < C; ++c) total += cnt_g[(size_t)c * E + e];
@@ -651,6 +677,8 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_scatter_kernel(cons
     __shared__ uint32_t bits[kDispatchThreads / 32][kMaxExperts];
     __shared__ int32_t wpre[kDispatchThreads / 32][kMaxExperts];
     const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
     for (int e = tid; e < E; e += kDispatchThreads) base[e] = base_g[(size_t)c * E + e];
     __syncthreads();
     const int t_end = (int)min((long long)(c + 1) * tpc, (long long)T);
@@ -769,6 +797,7 @@ __global__ void __launch_bounds__(256) preroute_kernel(const int32_t* __restrict
                                                        int32_t* __restrict__ idx, float* __restrict__ w,
                                                        int32_t* status) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    pdl_launch_dependents();
     if (i >= R) return;
     int e = __ldg(ids + i);
     if (e < 0 || e >= E) {
