@@ -634,37 +634,48 @@ def w4a8_moe_combine(y_rows: torch.Tensor, topk_w: torch.Tensor, out: Optional[t
 
 
 def w4a8_moe_dispatch(expert_ids: torch.Tensor, E: int, status: Optional[torch.Tensor] = None):
-    """(offsets int32 [E + 1], perm int32 [P], inv int32 [P]) of expert_ids int32
-    (P elements in any shape): the stable order of the rows by expert, as the
+    """(offsets int32 [E + 1], perm int32 [P], inv int32 [P]) of expert_ids (P
+    integers in any shape): the stable order of the rows by expert, as the
     grouped products take them.  perm[position] = row, inv[row] = position."""
     L = load_library()
-    _need_cuda(expert_ids)
-    dev = expert_ids.device
+    where = "w4a8_moe_dispatch"
+    if not expert_ids.is_cuda or expert_ids.dtype.is_floating_point:
+        _refuse(where, "expert_ids must be integers on a CUDA device")
+    index, E = expert_ids.get_device(), int(E)
+    _check_status(where, status, index)
     ids = expert_ids.to(torch.int32).contiguous()
     P = ids.numel()
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    perm = torch.empty(P, dtype=torch.int32, device=dev)
-    inv = torch.empty(P, dtype=torch.int32, device=dev)
-    need = int(L.w4a8_moe_dispatch_workspace_size(P, E))
-    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    _launch(dev, "w4a8_moe_dispatch", L.w4a8_moe_dispatch, ids.data_ptr(), P, int(E), offsets.data_ptr(),
-            perm.data_ptr(), inv.data_ptr(), ws.data_ptr(), ws.numel(), _addr(status))
+    offsets = ids.new_empty(max(E + 1, 0))
+    perm = ids.new_empty(P)
+    inv = ids.new_empty(P)
+    ws = _scratch(None, int(L.w4a8_moe_dispatch_workspace_size(P, E)), ids)
+    _launch(index, where, L.w4a8_moe_dispatch, ids.data_ptr(), P, E, offsets.data_ptr(), perm.data_ptr(),
+            inv.data_ptr(), *_scratch_args(ws), _addr(status))
     return offsets, perm, inv
 
 
 # -------------------------------------------------------- grouped products --
 
+# The host side of a call of single tokens takes about as long as its kernels,
+# so the checks below read each property once and compare device indexes, not
+# device objects.
+
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _launch(dev: torch.device, where: str, fn, *args):
-    """One library call on the current stream of `dev`, with `dev` current."""
-    if torch.cuda.current_device() == dev.index:
-        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+# The current stream's handle, without the Stream object around it where torch offers that.
+_current_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                 lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(index: int, where: str, fn, *args):
+    """One library call on the current stream of device `index`, with that device current."""
+    if torch.cuda.current_device() == index:
+        code = fn(*args, _current_stream_handle(index))
     else:
-        with torch.cuda.device(dev):
-            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(index):
+            code = fn(*args, _current_stream_handle(index))
     if code != 0:
         raise W4A8Error(code, where)
 
@@ -673,53 +684,58 @@ def _refuse(where: str, what: str):
     raise W4A8Error(1, f"{where}: {what}")
 
 
-def _scratch(workspace: Optional[torch.Tensor], need: int, dev: torch.device):
-    """(address, bytes) of a scratch buffer of at least `need` bytes, and the tensor that owns it."""
-    if workspace is not None and workspace.device == dev and workspace.is_contiguous():
-        have = workspace.numel() * workspace.element_size()
-        if have >= need:
-            return workspace.data_ptr(), have, workspace
-    if need == 0:
-        return None, 0, None
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    return workspace.data_ptr(), need, workspace
+def _scratch(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor):
+    """A scratch buffer of at least `need` bytes on the device of `like` (None when none is needed)."""
+    if (workspace is not None and workspace.get_device() == like.get_device() and workspace.is_contiguous()
+            and workspace.numel() * workspace.element_size() >= need):
+        return workspace
+    return like.new_empty(need, dtype=torch.uint8) if need else None
 
 
-def _check_status(where: str, status, dev):
-    if status is not None and (status.dtype != torch.int32 or status.device != dev):
-        _refuse(where, f"status must be int32 on {dev}")
+def _scratch_args(ws: Optional[torch.Tensor]):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def _check_status(where: str, status, index):
+    if status is not None and (status.dtype != torch.int32 or status.get_device() != index):
+        _refuse(where, "status must be int32 on the rows' device")
 
 
 def _check_grouped(where: str, x, dtype, offsets, w, out, status):
     """The shape and device rules every grouped product shares; returns
-    (device, rows, row pitch of x, out, row pitch of out)."""
-    if not x.is_cuda or x.dim() != 2 or x.dtype != dtype or x.stride(1) != 1:
+    (device index, rows, row pitch of x, out, row pitch of out)."""
+    if x.dtype != dtype or x.dim() != 2 or x.stride(1) != 1 or not x.is_cuda:
         _refuse(where, f"rows must be a {dtype} matrix [R, K] with unit column stride on a CUDA device")
-    dev, E, N = x.device, w.experts, w.desc.N
+    index, E, d = x.get_device(), w.experts, w.desc
+    R, K = x.shape
+    N = d.N
     if E <= 0:
         _refuse(where, "takes stacked expert weights")
-    R, K = x.shape
-    if K != w.desc.K:
-        _refuse(where, f"rows have {K} columns, the weight {w.desc.K} rows")
-    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or offsets.device != dev or not offsets.is_contiguous():
-        _refuse(where, f"offsets must be contiguous int32 [E + 1] on {dev}")
+    if K != d.K:
+        _refuse(where, f"rows have {K} columns, the weight {d.K} rows")
+    if (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() != E + 1
+            or offsets.get_device() != index or not offsets.is_contiguous()):
+        _refuse(where, "offsets must be contiguous int32 [E + 1] on the rows' device")
     if out is None:
-        out, pitch = torch.empty(R, N, dtype=torch.bfloat16, device=dev), N
+        out, pitch = x.new_empty((R, N), dtype=torch.bfloat16), N
     else:
         # a one-row matrix may carry any row stride
         pitch = out.stride(0) if R > 1 and out.dim() == 2 else N
-        if out.dtype != torch.bfloat16 or out.shape != (R, N) or out.device != dev or out.stride(1) != 1 or pitch < N:
-            _refuse(where, f"out must be bf16 [R, N] with unit column stride on {dev}")
-    _check_status(where, status, dev)
-    return dev, R, x.stride(0) if R > 1 else K, out, pitch
+        if (out.dtype != torch.bfloat16 or out.shape != (R, N) or out.get_device() != index or out.stride(1) != 1
+                or pitch < N):
+            _refuse(where, "out must be bf16 [R, N] with unit column stride on the rows' device")
+    if status is not None:
+        _check_status(where, status, index)
+    return index, R, x.stride(0) if R > 1 else K, out, pitch
 
 
-def _check_w8(where: str, w: PackedW8, dev):
+def _check_w8(where: str, w: PackedW8, index: int):
     q, s, d, E = w.q_w, w.s_w, w.desc, w.experts
-    if q.dtype != torch.int8 or q.shape != (E, d.N, d.K) or not q.is_contiguous() or q.device != dev:
-        _refuse(where, f"q_w must be contiguous int8 [E, N, K] on {dev}")
-    if s.dtype != torch.float32 or s.shape != (E, d.N) or not s.is_contiguous() or s.device != dev:
-        _refuse(where, f"s_w must be contiguous fp32 [E, N] on {dev}")
+    N = d.N
+    if q.dtype != torch.int8 or q.shape != (E, N, d.K) or not q.is_contiguous() or q.get_device() != index:
+        _refuse(where, "q_w must be contiguous int8 [E, N, K] on the rows' device")
+    if s.dtype != torch.float32 or s.shape != (E, N) or not s.is_contiguous() or s.get_device() != index:
+        _refuse(where, "s_w must be contiguous fp32 [E, N] on the rows' device")
 
 
 def w8a8_grouped_workspace_size(R: int, w: PackedW8) -> int:
@@ -735,16 +751,16 @@ def w8a8_grouped_gemm(qx: torch.Tensor, s_x: torch.Tensor, offsets: torch.Tensor
     they are in `out` (uninitialised when `out` is not given)."""
     L = load_library()
     where = "w8a8_grouped_gemm"
-    dev, R, pitch, out, ldy = _check_grouped(where, qx, torch.int8, offsets, w, out, status)
+    index, R, pitch, out, ldy = _check_grouped(where, qx, torch.int8, offsets, w, out, status)
     if pitch != w.desc.K:
         _refuse(where, "qx must be contiguous")
-    if s_x.dtype != torch.float32 or s_x.numel() != R or not s_x.is_contiguous() or s_x.device != dev:
-        _refuse(where, f"s_x must be contiguous fp32 [R] on {dev}")
-    _check_w8(where, w, dev)
+    if s_x.dtype != torch.float32 or s_x.numel() != R or not s_x.is_contiguous() or s_x.get_device() != index:
+        _refuse(where, "s_x must be contiguous fp32 [R] on the rows' device")
+    _check_w8(where, w, index)
     d = ctypes.byref(w.desc)
-    ws, ws_bytes, _keep = _scratch(workspace, L.w8a8_grouped_workspace_size(R, w.experts, d), dev)
-    _launch(dev, where, L.w8a8_grouped_gemm, qx.data_ptr(), s_x.data_ptr(), offsets.data_ptr(), R, w.experts,
-            w.q_w.data_ptr(), w.s_w.data_ptr(), d, out.data_ptr(), ldy, ws, ws_bytes, _addr(status))
+    ws = _scratch(workspace, L.w8a8_grouped_workspace_size(R, w.experts, d), qx)
+    _launch(index, where, L.w8a8_grouped_gemm, qx.data_ptr(), s_x.data_ptr(), offsets.data_ptr(), R, w.experts,
+            w.q_w.data_ptr(), w.s_w.data_ptr(), d, out.data_ptr(), ldy, *_scratch_args(ws), _addr(status))
     return out
 
 
@@ -760,12 +776,12 @@ def w8a8_grouped_linear(X: torch.Tensor, offsets: torch.Tensor, w: PackedW8, out
     belong to no expert are not read."""
     L = load_library()
     where = "w8a8_grouped_linear"
-    dev, R, pitch, out, ldy = _check_grouped(where, X, torch.bfloat16, offsets, w, out, status)
-    _check_w8(where, w, dev)
+    index, R, pitch, out, ldy = _check_grouped(where, X, torch.bfloat16, offsets, w, out, status)
+    _check_w8(where, w, index)
     d = ctypes.byref(w.desc)
-    ws, ws_bytes, _keep = _scratch(workspace, L.w8a8_grouped_linear_workspace_size(R, w.experts, d), dev)
-    _launch(dev, where, L.w8a8_grouped_linear, X.data_ptr(), R, pitch, offsets.data_ptr(), w.experts,
-            w.q_w.data_ptr(), w.s_w.data_ptr(), d, out.data_ptr(), ldy, ws, ws_bytes, _addr(status))
+    ws = _scratch(workspace, L.w8a8_grouped_linear_workspace_size(R, w.experts, d), X)
+    _launch(index, where, L.w8a8_grouped_linear, X.data_ptr(), R, pitch, offsets.data_ptr(), w.experts,
+            w.q_w.data_ptr(), w.s_w.data_ptr(), d, out.data_ptr(), ldy, *_scratch_args(ws), _addr(status))
     return out
 
 
@@ -782,20 +798,22 @@ def w4a16_grouped_gemm(X: torch.Tensor, offsets: torch.Tensor, w: PackedWeight, 
     no expert are left as they are in `out`."""
     L = load_library()
     where = "w4a16_grouped_gemm"
-    dev, R, pitch, out, ldy = _check_grouped(where, X, torch.bfloat16, offsets, w, out, status)
+    index, R, pitch, out, ldy = _check_grouped(where, X, torch.bfloat16, offsets, w, out, status)
     E, d, packed, s_w, z = w.experts, w.desc, w.packed, w.s_w, w.z
-    groups = (E, d.K // d.group if d.group > 0 else 0, d.N)
-    if (packed.dtype != torch.uint8 or packed.numel() != E * d.K * d.N // 2 or not packed.is_contiguous()
-            or packed.device != dev):
-        _refuse(where, f"packed must be contiguous uint8 [E, K * N / 2] on {dev}")
-    if s_w.dtype != torch.float32 or s_w.shape != groups or not s_w.is_contiguous() or s_w.device != dev:
-        _refuse(where, f"s_w must be contiguous fp32 [E, G, N] on {dev}")
-    if z is not None and (z.dtype != torch.uint8 or z.shape != groups or not z.is_contiguous() or z.device != dev):
-        _refuse(where, f"z must be contiguous uint8 [E, G, N] on {dev}")
+    K, N, group = d.K, d.N, d.group
+    groups = (E, K // group if group > 0 else 0, N)
+    if (packed.dtype != torch.uint8 or packed.numel() != E * K * N // 2 or not packed.is_contiguous()
+            or packed.get_device() != index):
+        _refuse(where, "packed must be contiguous uint8 [E, K * N / 2] on the rows' device")
+    if s_w.dtype != torch.float32 or s_w.shape != groups or not s_w.is_contiguous() or s_w.get_device() != index:
+        _refuse(where, "s_w must be contiguous fp32 [E, G, N] on the rows' device")
+    if z is not None and (z.dtype != torch.uint8 or z.shape != groups or not z.is_contiguous()
+                          or z.get_device() != index):
+        _refuse(where, "z must be contiguous uint8 [E, G, N] on the rows' device")
     d = ctypes.byref(d)
-    ws, ws_bytes, _keep = _scratch(workspace, L.w4a16_grouped_workspace_size(R, E, d), dev)
-    _launch(dev, where, L.w4a16_grouped_gemm, X.data_ptr(), R, pitch, offsets.data_ptr(), E, packed.data_ptr(),
-            s_w.data_ptr(), _addr(z), d, out.data_ptr(), ldy, ws, ws_bytes, _addr(status))
+    ws = _scratch(workspace, L.w4a16_grouped_workspace_size(R, E, d), X)
+    _launch(index, where, L.w4a16_grouped_gemm, X.data_ptr(), R, pitch, offsets.data_ptr(), E, packed.data_ptr(),
+            s_w.data_ptr(), _addr(z), d, out.data_ptr(), ldy, *_scratch_args(ws), _addr(status))
     return out
 
 
@@ -813,32 +831,33 @@ def w8a8_moe_grouped_gemm(X: torch.Tensor, logits: torch.Tensor, topk: int, w1: 
     Returns dict(out, topk_idx, topk_w, expert_offsets, workspace)."""
     L = load_library()
     where = "w8a8_moe_grouped_gemm"
-    dev = X.device
-    if (not X.is_cuda or X.dim() != 2 or logits.dim() != 2 or X.dtype != torch.bfloat16
-            or logits.dtype != torch.float32 or logits.device != dev or logits.shape[0] != X.shape[0]):
+    if (X.dtype != torch.bfloat16 or logits.dtype != torch.float32 or X.dim() != 2 or logits.dim() != 2
+            or not X.is_cuda or logits.get_device() != X.get_device() or logits.shape[0] != X.shape[0]):
         _refuse(where, "X must be bf16 [T, H] and logits fp32 [T, E] on one CUDA device")
+    index = X.get_device()
     T, H = X.shape
     E, topk = logits.shape[1], int(topk)
     if w1.experts != E or w2.experts != E or w1.desc.K != H:
         _refuse(where, "w1 and w2 must stack E experts for H")
-    _check_w8(where, w1, dev)
-    _check_w8(where, w2, dev)
-    _check_status(where, status, dev)
+    _check_w8(where, w1, index)
+    _check_w8(where, w2, index)
+    _check_status(where, status, index)
     X, logits = X.contiguous(), logits.contiguous()
     if out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
-    elif out.dtype != torch.bfloat16 or out.shape != (T, H) or not out.is_contiguous() or out.device != dev:
-        _refuse(where, f"out must be contiguous bf16 [T, H] on {dev}")
-    idx = torch.empty(T, max(topk, 0), dtype=torch.int32, device=dev)
-    pw = torch.empty(T, max(topk, 0), dtype=torch.float32, device=dev)
-    offs = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        out = X.new_empty((T, H))
+    elif (out.dtype != torch.bfloat16 or out.shape != (T, H) or not out.is_contiguous()
+          or out.get_device() != index):
+        _refuse(where, "out must be contiguous bf16 [T, H] on the rows' device")
+    idx = X.new_empty((T, max(topk, 0)), dtype=torch.int32)
+    pw = logits.new_empty((T, max(topk, 0)))
+    offs = X.new_empty(E + 1, dtype=torch.int32)
     if T == 0:
         offs.zero_()
     d1, d2 = ctypes.byref(w1.desc), ctypes.byref(w2.desc)
-    ws, ws_bytes, workspace = _scratch(workspace, L.w8a8_moe_workspace_size(T, E, topk, d1, d2), dev)
-    _launch(dev, where, L.w8a8_moe_grouped_gemm, X.data_ptr(), logits.data_ptr(), T, E, topk, w1.q_w.data_ptr(),
+    workspace = _scratch(workspace, L.w8a8_moe_workspace_size(T, E, topk, d1, d2), X)
+    _launch(index, where, L.w8a8_moe_grouped_gemm, X.data_ptr(), logits.data_ptr(), T, E, topk, w1.q_w.data_ptr(),
             w1.s_w.data_ptr(), d1, w2.q_w.data_ptr(), w2.s_w.data_ptr(), d2, out.data_ptr(), idx.data_ptr(),
-            pw.data_ptr(), offs.data_ptr(), ws, ws_bytes, _addr(status))
+            pw.data_ptr(), offs.data_ptr(), *_scratch_args(workspace), _addr(status))
     return dict(out=out, topk_idx=idx, topk_w=pw, expert_offsets=offs, workspace=workspace)
 
 
@@ -848,25 +867,26 @@ def w8a8_moe_experts(X: torch.Tensor, expert_ids: torch.Tensor, w1: PackedW8, w2
     """y bf16 [R, H]: row r of X bf16 [R, H] through INT8 expert expert_ids[r] (unweighted)."""
     L = load_library()
     where = "w8a8_moe_experts"
-    dev = X.device
-    if not X.is_cuda or X.dim() != 2 or X.dtype != torch.bfloat16:
+    if X.dtype != torch.bfloat16 or X.dim() != 2 or not X.is_cuda:
         _refuse(where, "X must be bf16 [R, H] on a CUDA device")
+    index = X.get_device()
     R, H = X.shape
     E = w1.experts
-    if expert_ids.device != dev or expert_ids.numel() != R or expert_ids.dtype.is_floating_point:
-        _refuse(where, f"expert_ids must be R integers on {dev}")
+    if expert_ids.get_device() != index or expert_ids.numel() != R or expert_ids.dtype.is_floating_point:
+        _refuse(where, "expert_ids must be R integers on the rows' device")
     if E <= 0 or w2.experts != E or w1.desc.K != H:
         _refuse(where, "w1 and w2 must stack the same experts for H")
-    _check_w8(where, w1, dev)
-    _check_w8(where, w2, dev)
-    _check_status(where, status, dev)
+    _check_w8(where, w1, index)
+    _check_w8(where, w2, index)
+    _check_status(where, status, index)
     X, ids = X.contiguous(), expert_ids.to(torch.int32).contiguous()
     if out is None:
-        out = torch.empty(R, H, dtype=torch.bfloat16, device=dev)
-    elif out.dtype != torch.bfloat16 or out.shape != (R, H) or not out.is_contiguous() or out.device != dev:
-        _refuse(where, f"out must be contiguous bf16 [R, H] on {dev}")
+        out = X.new_empty((R, H))
+    elif (out.dtype != torch.bfloat16 or out.shape != (R, H) or not out.is_contiguous()
+          or out.get_device() != index):
+        _refuse(where, "out must be contiguous bf16 [R, H] on the rows' device")
     d1, d2 = ctypes.byref(w1.desc), ctypes.byref(w2.desc)
-    ws, ws_bytes, _keep = _scratch(workspace, L.w8a8_moe_experts_workspace_size(R, E, d1, d2), dev)
-    _launch(dev, where, L.w8a8_moe_experts, X.data_ptr(), ids.data_ptr(), R, E, w1.q_w.data_ptr(), w1.s_w.data_ptr(),
-            d1, w2.q_w.data_ptr(), w2.s_w.data_ptr(), d2, out.data_ptr(), ws, ws_bytes, _addr(status))
+    ws = _scratch(workspace, L.w8a8_moe_experts_workspace_size(R, E, d1, d2), X)
+    _launch(index, where, L.w8a8_moe_experts, X.data_ptr(), ids.data_ptr(), R, E, w1.q_w.data_ptr(), w1.s_w.data_ptr(),
+            d1, w2.q_w.data_ptr(), w2.s_w.data_ptr(), d2, out.data_ptr(), *_scratch_args(ws), _addr(status))
     return out
