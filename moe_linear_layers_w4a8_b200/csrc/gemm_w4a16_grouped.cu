@@ -22,7 +22,7 @@ static int launch_w4a16_grouped_t(const CUtensorMap& tmap_x, const CUtensorMap& 
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kW16GThreads);
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -41,7 +41,7 @@ int launch_w4a16_grouped(int bn, bool sym, const CUtensorMap& tx, const CUtensor
         return sym ? launch_w4a16_grouped_t<B, true>(tx, txs, ts, tz, p, grid, stream)      \
                    : launch_w4a16_grouped_t<B, false>(tx, txs, ts, tz, p, grid, stream);
     switch (bn) {
-        W4A8_W16G(16) W4A8_W16G(32) W4A8_W16G(64) W4A8_W16G(128) W4A8_W16G(224)
+        W4A8_W16G(16) W4A8_W16G(32) W4A8_W16G(64) W4A8_W16G(128) W4A8_W16G(192)
     }
 #undef W4A8_W16G
     return 2;

@@ -12,25 +12,29 @@
 //   * Swap-AB: 128 weight columns are the MMA's rows, up to BN tokens its
 //     columns; its N is set to the tile's rows, and few rows take small
 //     activation boxes.
-//   * A stage is two k-blocks of 64: the dequantized bf16 weights (A) and the
-//     rows (B), both in the MMA's 128-byte swizzled layout.  One lane issues the
-//     eight MMAs of a stage between one wait and one commit: per k-block that
-//     costs it 250 cycles, with a wait and a commit for each half of that 600.
+//   * A unit is two k-blocks of 64.  The dequantized bf16 weights go straight
+//     to TMEM (the MMA's A operand: lane = column, 32 TMEM columns for a
+//     k-block), so they need neither shared memory nor a proxy fence; with A in
+//     shared memory the stores and the fence took 500 of a k-block's 2,400
+//     cycles (512 rows over 32 experts, K = 7168, N = 4096: 264 -> 245 us).
 //   * 16 warps dequantize, four teams of 4, k-blocks in turn, so that one team's
-//     waits, stores and proxy fence (500 of its 2400 cycles) overlap the others'
-//     arithmetic.  A thread takes one column's 64 k of a k-block: one scale,
-//     two 16-byte code chunks, eight 16-byte stores.  It gives the stage of
-//     packed weights back as soon as the codes are in its registers.
+//     waits and stores overlap the others' arithmetic.  A thread takes one
+//     column's 64 k of a k-block: one scale, two 16-byte code chunks.  It gives
+//     the stage of packed weights back as soon as the codes are in registers.
+//     (Six teams at 64 registers a thread: no faster.)
+//   * The producers and the MMA warp run converged, one lane issuing: a lone
+//     lane moves every descriptor and address to uniform registers one by one,
+//     135 cycles for each MMA instead of 32, 300 for each copy (245 -> 224 us
+//     from the producers, 310 -> 270 from the MMAs).
 //   * Bound by the dequantization: about 22 instructions for 8 weights, 13 of
-//     them integer ones at half rate (a mask as an immediate and 2^23 in a
-//     register: with a second constant for the flipped bit each mask cost one
-//     move more, 424 -> 369 us), plus 8 for the stores and hand-over.  Measured
-//     0.33 us per k-block of 64 and CTA at any number of rows, which is the time
-//     of the MMAs at 170 rows.
+//     them integer ones at half rate: 230 cycles of a k-block's 540 per CTA if
+//     nothing else ran (0.29 us at any number of rows, which is the time of the
+//     MMAs at 150).  A mask is an immediate and 2^23 a register; a second
+//     constant for the flipped bit cost each mask a move (424 -> 369 us, 24576
+//     rows over 64 experts, K = 2048, N = 2816).
 // Tried and taken out: a kernel on mma.sync whose lanes keep the weights they
-// dequantize (no shared memory between the two); its instructions for the
-// fragments outweighed the hand-over: 280 us against 259 (512 rows, 32 experts,
-// K = 7168, N = 4096, groups of 64).
+// dequantize; its fragment loads and group scales came to 1.5 instructions for
+// a weight more: 280 us.
 #pragma once
 
 #include <cstdint>
@@ -62,32 +66,35 @@ struct W16GroupedParams {
     unsigned long long wait_ns;
 };
 
-constexpr int kW16GThreads = 736;      // weight producer, MMA, 4 epilogue warps, 16 dequant warps, row producer
-constexpr int kW16GEpiWarp0 = 2;
-constexpr int kW16GDqWarp0 = 6;
-constexpr int kW16GDqWarps = 16;       // four teams of 4, k-blocks in turn; two teams fill a stage
-constexpr int kW16GTeams = 4;
-constexpr int kW16GXWarp = 22;
+constexpr int kW16GEpiWarp0 = 3;       // after the two producers and the MMA warp
+constexpr int kW16GDqWarp0 = 8;        // a multiple of 4: a warp's TMEM lanes follow from its number
 constexpr int kW16GKSW = 2;            // k-blocks of 64 per stage of packed weights: those of one pair of teams
 constexpr int kW16GSmall = 32;         // rows of the small activation box
 
 // Rows of the large activation box (one k-block) of a tile of bn rows.
-__host__ __device__ constexpr int w4a16_grouped_xrows(int bn) { return bn == 224 ? 112 : bn; }
+__host__ __device__ constexpr int w4a16_grouped_xrows(int bn) { return bn == 192 ? 96 : bn; }
 
 template <int BN>
 struct W16GCfg {
     static constexpr int XB = BN * 128;                    // one k-block of activations: BN rows x 64 k bf16
-    static constexpr int A_BYTES = 128 * 128;              // one k-block of bf16 weights: 128 columns x 64 k
-    static constexpr int STAGE = 2 * (A_BYTES + XB);       // two k-blocks: weights, then activations
-    static constexpr int NS = BN <= 32 ? 4 : 2;            // stages: unit % NS of every tile
+    static constexpr int STAGE = 2 * XB;                   // activations of two k-blocks
+    static constexpr int NS = BN <= 128 ? 4 : 2;           // stages: the CTA's units in turn
+    // Pairs of teams of 4 dequantizing warps; a pair fills a stage.  At most NS: a pair that is P units ahead
+    // has seen unit - P - NS released, and a barrier's parity tells two uses of a stage apart, not three.
+    static constexpr int PAIRS = 2;
+    static constexpr int DQ_WARPS = 8 * PAIRS;
+    static constexpr int THREADS = 32 * (kW16GDqWarp0 + DQ_WARPS);
+    static_assert(PAIRS <= NS, "a pair's lead");
     static constexpr int XROWS = w4a16_grouped_xrows(BN);  // rows of the large activation box
     static constexpr int KSW = kW16GKSW;
     static constexpr int PK_HALF = KSW * 2048;             // codes of one 64-column half
     static constexpr int W_S = 2 * PK_HALF;                // fp32 scales [KSW][128]
     static constexpr int W_Z = W_S + KSW * 512;            // zero-points [KSW][128]
     static constexpr int W_STAGE = W_Z + KSW * 128;
-    static constexpr int NW = 4;                                     // stages of packed weights: unit % NW of every tile
-    static constexpr int STG = BN == 224 ? 4 * 1024 : 4 * 2048;   // output staging: LB tokens x 32 columns per warp
+    // Stages of packed weights, the CTA's units in turn.  A multiple of PAIRS: a stage's readers are always the same
+    // pair, which has seen its last use (copies of different stages may land out of order).
+    static constexpr int NW = 2 * PAIRS;
+    static constexpr int STG = 4 * 1024;                   // output staging: 16 tokens x 32 columns per warp
     static constexpr int OFF_W = NS * STAGE;
     static constexpr int OFF_Y = OFF_W + NW * W_STAGE;
     static constexpr int OFF_BAR = OFF_Y + STG;
@@ -96,10 +103,13 @@ struct W16GCfg {
     static constexpr int TABLE = 3 * (kGroupedMaxExperts + 1) * 4;
     static constexpr int OFF_MISC = OFF_TABLE + TABLE;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
-    static constexpr uint32_t TMEM_COLS = BN == 224 ? 512 : 2 * BN;
+    // TMEM: two accumulators, then the dequantized weights: 64 columns (two k-blocks of 64 bf16) per stage
+    static constexpr int A_COL0 = 2 * BN;
+    static constexpr uint32_t TMEM_COLS = A_COL0 + 64 * NS <= 256 ? 256 : A_COL0 + 64 * NS <= 512 ? 512 : 1024;
+    static_assert(TMEM_COLS <= 512, "TMEM");
     static constexpr int SPLIT_GAIN = 3 + BN / 64;         // stages of 128 k (a partial tile is BN / 2 KB)
-    static constexpr int LB = BN == 224 || BN < 32 ? 16 : 32;   // tokens per epilogue batch
-    static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128 || BN == 224, "BN");
+    static constexpr int LB = 16;                        // tokens per epilogue batch
+    static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128 || BN == 192, "BN");
     static_assert(W_S % 128 == 0 && W_STAGE % 128 == 0, "TMA destinations");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -146,8 +156,20 @@ __device__ __forceinline__ void dequant_word32(uint32_t w, const NibblePairs<SYM
     hi[1] = pack_bf16x2(h2, h3);
 }
 
+// D[tmem] (+)= A[tmem] * B[smem]^T, bf16 x bf16 -> fp32, K = 16; the A tile
+// sits in TMEM (lane = row, 2 consecutive k per 32-bit column).
+__device__ __forceinline__ void mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 template <int BN, bool SYM>
-__global__ void __launch_bounds__(kW16GThreads, 1)
+__global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
     w4a16_grouped_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_xs,
                          const __grid_constant__ CUtensorMap tmap_s, const __grid_constant__ CUtensorMap tmap_z,
                          const W16GroupedParams p) {
@@ -176,10 +198,10 @@ __global__ void __launch_bounds__(kW16GThreads, 1)
         pdl_launch_dependents();
         for (int i = 0; i < C::NW; ++i) {
             mbar_init(&w_full[i], 1);
-            mbar_init(&w_empty[i], kW16GDqWarps / 2);
+            mbar_init(&w_empty[i], 8);
         }
         for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&full[i], kW16GDqWarps / 2 + 1);
+            mbar_init(&full[i], 8 + 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -214,84 +236,97 @@ __global__ void __launch_bounds__(kW16GThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------ producer: weight ring --
-        if (lane == 0) {
-            uint32_t phases = 0u;    // parity of every stage's next fill
-            uint32_t used = 0u;      // stages that have been filled
-            bool ok = true;
-            const int sg_rows = C::KSW >> kb_shift;
-            while (ok && walk.next(tile, u0, u1)) {
-                const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
-                const int halves = min(128, p.N - gt.nt * 128) / 64;
-                const uint8_t* codes = p.packed + gt.e * p.packed_estride;
-                for (int u = u0; u < u1; ++u) {
-                    const int kb = 2 * u, len = min(C::KSW, KB - kb);
-                    const int slot = u & (C::NW - 1);
-                    if (!wait_bounded(&w_empty[slot], ((phases >> slot) & 1u) ^ 1u, wc)) { ok = false; break; }
+        const bool leader = elect_one();
+        uint32_t phases = 0u;    // parity of every stage's next fill
+        uint32_t used = 0u;      // stages that have been filled
+        uint32_t seq = 0u;       // units of this CTA so far
+        bool ok = true;
+        const int sg_rows = C::KSW >> kb_shift;
+        while (ok && walk.next(tile, u0, u1)) {
+            const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
+            const int halves = min(128, p.N - gt.nt * 128) / 64;
+            const uint8_t* codes = p.packed + gt.e * p.packed_estride + (long long)gt.nt * 2 * KB * 2048;
+            for (int u = u0; u < u1; ++u, ++seq) {
+                const int kb = 2 * u, len = min(C::KSW, KB - kb);
+                const int slot = seq % C::NW;
+                ok = warp_wait_bounded(&w_empty[slot], ((phases >> slot) & 1u) ^ 1u, wc);
+                if (!ok) break;
+                if (leader) {
                     uint32_t bytes = halves * len * 2048 + sg_rows * 512;
                     if (!SYM) bytes += sg_rows * 128;
                     mbar_arrive_expect_tx(&w_full[slot], bytes);
                     uint8_t* st = smem + C::OFF_W + slot * C::W_STAGE;
                     // 64 columns x 32 k are 1 KB; a column block's chunks follow one another over all of K
-                    for (int hf = 0; hf < halves; ++hf)
-                        bulk_load(st + hf * C::PK_HALF, codes + ((long long)(gt.nt * 2 + hf) * KB + kb) * 2048,
-                                  len * 2048, &w_full[slot]);
+                    bulk_load(st, codes + (long long)kb * 2048, len * 2048, &w_full[slot]);
+                    if (halves == 2)
+                        bulk_load(st + C::PK_HALF, codes + (long long)(KB + kb) * 2048, len * 2048, &w_full[slot]);
                     const int g0 = gt.e * p.G + (kb >> kb_shift);
                     tma_load_2d(st + C::W_S, &tmap_s, &w_full[slot], gt.nt * 128, g0);
                     if (!SYM) tma_load_2d(st + C::W_Z, &tmap_z, &w_full[slot], gt.nt * 128, g0);
-                    used |= 1u << slot;
-                    phases ^= 1u << slot;
                 }
+                __syncwarp();
+                used |= 1u << slot;
+                phases ^= 1u << slot;
             }
-            // copies in flight land before the CTA leaves
+        }
+        // copies in flight land before the CTA leaves
+        if (leader) {
             WaitCtx wd = wc;
             volatile int no_abort = 0;
             wd.abort = &no_abort;
             for (int i = 0; i < C::NW; ++i)   // parity of a stage's last fill
                 if ((used >> i) & 1u) (void)wait_bounded(&w_full[i], ((phases >> i) & 1u) ^ 1u, wd);
         }
-    } else if (warp == kW16GXWarp) {
+        __syncwarp();
+    } else if (warp == 2) {
         // ------------------------------------------- producer: activations --
-        if (lane == 0) {
-            uint32_t phases = 0u, used = 0u;
-            bool ok = true;
-            while (ok && walk.next(tile, u0, u1)) {
-                const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
-                // few rows: one or two small boxes per k-block instead of the large ones
-                const bool small = C::XROWS > kW16GSmall && gt.rows <= (BN >= 128 ? 2 : 1) * kW16GSmall;
-                const int per = small ? kW16GSmall : C::XROWS;
-                const int boxes = gt.rows > per ? 2 : 1;
-                const CUtensorMap* map = small ? &tmap_xs : &tmap_x;
-                for (int u = u0; u < u1; ++u) {
-                    const int kb = 2 * u, len = min(2, KB - kb);
-                    const int slot = u & (C::NS - 1);
-                    if (!wait_bounded(&empty[slot], ((phases >> slot) & 1u) ^ 1u, wc)) { ok = false; break; }
-                    uint8_t* st = smem + slot * C::STAGE + 2 * C::A_BYTES;
+        const bool leader = elect_one();
+        uint32_t phases = 0u, used = 0u, seq = 0u;
+        bool ok = true;
+        while (ok && walk.next(tile, u0, u1)) {
+            const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
+            // few rows: one or two small boxes per k-block instead of the large ones
+            const bool small = C::XROWS > kW16GSmall && gt.rows <= (BN >= 128 ? 2 : 1) * kW16GSmall;
+            const int per = small ? kW16GSmall : C::XROWS;
+            const int boxes = gt.rows > per ? 2 : 1;
+            const CUtensorMap* map = small ? &tmap_xs : &tmap_x;
+            for (int u = u0; u < u1; ++u, ++seq) {
+                const int kb = 2 * u, len = min(2, KB - kb);
+                const int slot = seq % C::NS;
+                ok = warp_wait_bounded(&empty[slot], ((phases >> slot) & 1u) ^ 1u, wc);
+                if (!ok) break;
+                if (leader) {
+                    uint8_t* st = smem + slot * C::STAGE;
                     mbar_arrive_expect_tx(&full[slot], len * boxes * (per * 128));
                     for (int i = 0; i < len; ++i, st += C::XB) {
                         tma_load_3d(st, map, &full[slot], 0, gt.row0, kb + i);
                         if (boxes == 2) tma_load_3d(st + per * 128, map, &full[slot], 0, gt.row0 + per, kb + i);
                     }
-                    phases ^= 1u << slot;
-                    used |= 1u << slot;
                 }
+                __syncwarp();
+                phases ^= 1u << slot;
+                used |= 1u << slot;
             }
-            // copies in flight land before the CTA leaves.  A stage completes with its weights; when the CTA gives
-            // up they may never come, and the wait runs to its limit.
+        }
+        // copies in flight land before the CTA leaves.  A stage completes with its weights; when the CTA gives
+        // up they may never come, and the wait runs to its limit.
+        if (leader) {
             WaitCtx wd = wc;
             volatile int no_abort = 0;
             wd.abort = &no_abort;
             for (int i = 0; i < C::NS; ++i)
                 if ((used >> i) & 1u) (void)wait_bounded(&full[i], ((phases >> i) & 1u) ^ 1u, wd);
         }
+        __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issue --
         // The whole warp runs the loop and one lane issues: with every value
         // uniform over the warp, an MMA's descriptors sit in uniform registers
-        // instead of being moved there one by one (135 -> 32 cycles for each).
+        // instead of being moved there one by one.
         {
             const bool leader = elect_one();
             Ring rc;
-            uint32_t phases = 0u;
+            uint32_t phases = 0u, seq = 0u;
             bool ok = true;
             while (ok && walk.next(tile, u0, u1)) {
                 const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
@@ -299,21 +334,21 @@ __global__ void __launch_bounds__(kW16GThreads, 1)
                 if (!warp_wait_bounded(&acc_empty[rc.idx], rc.phase ^ 1u, wc)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + rc.idx * BN;
-                for (int u = u0; u < u1; ++u) {
-                    const int slot = u & (C::NS - 1);
+                for (int u = u0; u < u1; ++u, ++seq) {
+                    const int slot = seq % C::NS;
                     if (!warp_wait_bounded(&full[slot], (phases >> slot) & 1u, wc)) { ok = false; break; }
                     tc_fence_after();
                     if (leader) {
                         const uint32_t st = smem_u32(smem + slot * C::STAGE);
-                        const uint64_t adesc = umma_desc_kmajor(st, 128);
-                        const uint64_t bdesc = umma_desc_kmajor(st + 2 * C::A_BYTES, 128);
+                        const uint32_t a = tmem_base + C::A_COL0 + slot * 64;
+                        const uint64_t bdesc = umma_desc_kmajor(st, 128);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_bf16(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, (u > u0 || kk > 0) ? 1u : 0u);
+                            mma_bf16_tmem_a(d_tmem, a + 8 * kk, bdesc + 2 * kk, idesc, (u > u0 || kk > 0) ? 1u : 0u);
                         if (2 * u + 1 < KB) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_bf16(d_tmem, adesc + (C::A_BYTES >> 4) + 2 * kk, bdesc + (C::XB >> 4) + 2 * kk, idesc, 1u);
+                                mma_bf16_tmem_a(d_tmem, a + 32 + 8 * kk, bdesc + (C::XB >> 4) + 2 * kk, idesc, 1u);
                         }
                         tc_commit(&empty[slot]);
                     }
@@ -335,30 +370,30 @@ __global__ void __launch_bounds__(kW16GThreads, 1)
             }
             __syncwarp();
         }
-    } else if (warp >= kW16GDqWarp0 && warp < kW16GDqWarp0 + kW16GDqWarps) {
+    } else if (warp >= kW16GDqWarp0) {
         // ----------------------------------------------------- dequantize --
         // The teams take k-blocks in turn, so that one's waits and hand-over
         // overlap the others' arithmetic.  A thread takes one column's 64 k:
         // they lie in one group, so its scale is set up once for 64 weights.
-        const int dt = threadIdx.x - kW16GDqWarp0 * 32;  // 0..511
-        const int team = dt >> 7;
-        const int r = dt & 127;                          // weight column within the tile = A row
+        const int team = (warp - kW16GDqWarp0) >> 2;
+        const int r = (warp & 3) * 32 + lane;            // weight column within the tile = A row = TMEM lane
         const int hf = r >> 6;
-        // unit i of the row lies at row ^ (i << 4) (128-byte swizzle)
-        const uint32_t row0 = smem_u32(smem) + (team & 1) * C::A_BYTES + r * 128 + ((r & 7) << 4);
+        const uint32_t a_tmem = tmem_base + (((uint32_t)(warp & 3) * 32) << 16) + C::A_COL0 + (team & 1) * 32;
         const int j = team & 1;                          // this team's k-block of its pair's two
         const uint32_t off_c = hf * C::PK_HALF + j * 2048 + (r & 63) * 16;
         const uint32_t off_s = C::W_S + ((j >> kb_shift) * 128 + r) * 4, off_z = C::W_Z + (j >> kb_shift) * 128 + r;
-        uint32_t phases = 0u, w_phases = 0u;             // of the stages, of those of packed weights
+        uint32_t seq = 0u;                               // units of this CTA so far
+        uint32_t own = team >> 1;                        // the pair's next among them: every C::PAIRS-th
         bool ok = true;
         while (ok && walk.next(tile, u0, u1)) {
             const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
             const bool valid = hf * 64 < min(128, p.N - gt.nt * 128);
-            for (int u = u0 + ((u0 ^ (team >> 1)) & 1); u < u1; u += 2) {   // the pair's stages: u % 2 = team / 2
-                const int slot = u & (C::NW - 1);
-                ok = warp_wait_bounded(&w_full[slot], (w_phases >> slot) & 1u, wc);
+            const uint32_t end = seq + (uint32_t)(u1 - u0);
+            for (; own < end; own += C::PAIRS) {
+                const int u = u0 + (int)(own - seq);
+                const uint32_t slot = own % C::NW;
+                ok = warp_wait_bounded(&w_full[slot], (own / C::NW) & 1u, wc);
                 if (!ok) break;
-                w_phases ^= 1u << slot;
                 // everything this thread needs of the stage, which is then free again
                 const bool mine = 2 * u + j < KB;        // warp-uniform
                 const uint8_t* st = smem + C::OFF_W + slot * C::W_STAGE;
@@ -373,35 +408,31 @@ __global__ void __launch_bounds__(kW16GThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&w_empty[slot]);
-                uint4 out[8];
-                if (mine) {
-                    NibblePairs<SYM> q;
-                    q.set(sv, zv);
-                    dequant_word32<SYM>(c0.x, q, &out[0].x, &out[2].x);
-                    dequant_word32<SYM>(c0.y, q, &out[0].z, &out[2].z);
-                    dequant_word32<SYM>(c0.z, q, &out[1].x, &out[3].x);
-                    dequant_word32<SYM>(c0.w, q, &out[1].z, &out[3].z);
-                    dequant_word32<SYM>(c1.x, q, &out[4].x, &out[6].x);
-                    dequant_word32<SYM>(c1.y, q, &out[4].z, &out[6].z);
-                    dequant_word32<SYM>(c1.z, q, &out[5].x, &out[7].x);
-                    dequant_word32<SYM>(c1.w, q, &out[5].z, &out[7].z);
-                }
-                const int as = u & (C::NS - 1);
-                ok = warp_wait_bounded(&empty[as], ((phases >> as) & 1u) ^ 1u, wc);
+                const uint32_t as = own % C::NS;
+                uint32_t out[16];                        // 32 k of the column, bf16 pairs in k order
+                NibblePairs<SYM> q;
+                q.set(sv, zv);
+                auto chunk = [&](const uint4& c) {
+                    dequant_word32<SYM>(c.x, q, out, out + 8);
+                    dequant_word32<SYM>(c.y, q, out + 2, out + 10);
+                    dequant_word32<SYM>(c.z, q, out + 4, out + 12);
+                    dequant_word32<SYM>(c.w, q, out + 6, out + 14);
+                };
+                if (mine) chunk(c0);
+                ok = warp_wait_bounded(&empty[as], ((own / C::NS) & 1u) ^ 1u, wc);
                 if (!ok) break;
-                phases ^= 1u << as;
                 if (mine) {
-                    const uint32_t a_row = row0 + as * C::STAGE;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a_row ^ (i << 4)), "r"(out[i].x),
-                                     "r"(out[i].y), "r"(out[i].z), "r"(out[i].w)
-                                     : "memory");
-                    fence_proxy_async_smem();  // generic-proxy writes -> visible to the tensor core
+                    tc_fence_after();
+                    tmem_st32<16>(a_tmem + as * 64, out);
+                    chunk(c1);
+                    tmem_st32<16>(a_tmem + as * 64 + 16, out);
+                    tmem_wait_st();
                 }
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[as]);
             }
+            seq = end;
         }
     } else if (warp >= kW16GEpiWarp0 && warp < kW16GEpiWarp0 + 4) {
         // ------------------------------------------------------- epilogue --
@@ -512,7 +543,7 @@ __global__ void __launch_bounds__(kW16GThreads, 1)
 }
 
 // Launches the grouped W4A16 tile kernel for a tile of BN in {16, 32, 64, 128,
-// 224} rows (defined in gemm_w4a16_grouped.cu).  tmap_xs: boxes of kW16GSmall
+// 192} rows (defined in gemm_w4a16_grouped.cu).  tmap_xs: boxes of kW16GSmall
 // rows x one k-block.  Status codes as in w4a8.h.
 int launch_w4a16_grouped(int bn, bool sym, const CUtensorMap& tmap_x, const CUtensorMap& tmap_xs,
                          const CUtensorMap& tmap_s, const CUtensorMap& tmap_z, const W16GroupedParams& p, int grid,

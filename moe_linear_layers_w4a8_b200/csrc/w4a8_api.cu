@@ -755,15 +755,14 @@ W8GroupedPlan plan_w16_grouped(long long R, int E, int N, int K, int sms) {
     pl.n_tiles = (N + 127) / 128;
     pl.KB = (K / 64 + 1) / 2;
     pl.grid = sms <= 0 ? 1 : (sms > 254 ? 254 : sms);
-    const int sizes[5] = {224, 128, 64, 32, 16};
+    const int sizes[5] = {192, 128, 64, 32, 16};
     // A taller tile dequantizes a weight fewer times.  512 rows over 32 uneven
-    // experts: 16, 64, 128, 224 rows 443, 293, 287, 259 us; 777 rows over 8 of
-    // 10, N = 1088: 32.9, 14.0, 14.8, 16.2 us; 6 experts of one row: 15.2, 16.7,
-    // 16.3, 16.1 us.
+    // experts: 16, 64, 128, 192 rows 335, 247, 245, 224 us; 777 rows over 8 of
+    // 10, N = 1088: 29.4, 12.3, 13.4, 15.4 us; 6 experts of one row: 13.7 to 14.2.
     pl.bn = grouped_bn(R, E, pl.n_tiles, pl.grid, sizes, 5, 16);
     const long long fewest = ((R + pl.bn - 1) / pl.bn) * pl.n_tiles;
-    if (pl.KB > 1 && fewest < 4LL * pl.grid) {
-        pl.split_tiles = 4 * pl.grid;
+    if (pl.KB > 1 && fewest < 16LL * pl.grid) {
+        pl.split_tiles = 16 * pl.grid;
         pl.counts_off = (size_t)2 * pl.grid * pl.bn * 128 * sizeof(float);
         pl.ws_bytes = pl.counts_off + (size_t)pl.split_tiles * sizeof(unsigned long long);
     }
