@@ -297,19 +297,22 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
 
     if (warp == 0 || warp == kW8GXWarp) {
         // ------------------------------------------------------ producers --
-        if (lane == 0) {
-            const bool is_w = warp == 0;
-            if (!is_w) pdl_wait_prerequisites();
-            uint64_t* full = is_w ? w_full : x_full;
-            Ring rs;
-            long long issued = 0;
-            bool ok = true;
-            while (ok && walk.next(tile, kb0, kb1)) {
-                const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
-                const int boxes = gt.rows > C::XBOX ? 2 : 1;
-                const int col = gt.nt * (GATEUP ? 128 : 128 * p.halves);
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!wait_bounded(&empty[rs.idx], rs.phase ^ 1u, wc)) { ok = false; break; }
+        // Converged, one lane issuing, like the MMA warps below.
+        const bool is_w = warp == 0;
+        const bool leader = elect_one();
+        uint64_t* full = is_w ? w_full : x_full;
+        if (!is_w) pdl_wait_prerequisites();
+        Ring rs;
+        long long issued = 0;
+        bool ok = true;
+        while (ok && walk.next(tile, kb0, kb1)) {
+            const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
+            const int boxes = gt.rows > C::XBOX ? 2 : 1;
+            const int col = gt.nt * (GATEUP ? 128 : 128 * p.halves);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = warp_wait_bounded(&empty[rs.idx], rs.phase ^ 1u, wc);
+                if (!ok) break;
+                if (leader) {
                     uint8_t* st = smem + rs.idx * C::STAGE;
                     if (is_w) {
                         mbar_arrive_expect_tx(&full[rs.idx], p.halves * (C::A_STAGE / 2));
@@ -321,11 +324,14 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
                         if (boxes == 2)
                             tma_load_2d(st + C::XBOX * 128, &tmap_x, &full[rs.idx], kb * 128, gt.row0 + C::XBOX);
                     }
-                    rs.next(C::NST);
-                    ++issued;
                 }
+                __syncwarp();
+                rs.next(C::NST);
+                ++issued;
             }
-            // copies in flight land before the CTA leaves
+        }
+        // copies in flight land before the CTA leaves
+        if (leader) {
             WaitCtx wd = wc;
             volatile int no_abort = 0;
             wd.abort = &no_abort;
@@ -335,6 +341,7 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
                 (void)wait_bounded(&full[d.idx], d.phase, wd);
             }
         }
+        __syncwarp();
     } else if (warp == 1 || warp == kW8GMma2Warp) {
         // ------------------------------------------------------ MMA issue --
         // One warp for each of the pair's accumulators: what a warp spends between
