@@ -336,7 +336,7 @@ W4A8_API size_t w8a8_grouped_workspace_size(int R, int E, const w4a8_wdesc* w);
 
 /* w8a8_grouped_gemm — the grouped product of quantized rows.
  * qx        device int8 [R][K], 16-byte aligned; s_x device fp32 [R].
- * Y         device bf16 [R][ldy], ldy >= N.
+ * Y         device bf16 [R][ldy], ldy >= N; overlaps no input.
  * workspace device scratch, 16-byte aligned, at least
  *           w8a8_grouped_workspace_size(R, E, w) bytes; needs no
  *           initialisation.  No CTA waits for another, so nothing here depends
@@ -412,7 +412,7 @@ W4A8_API size_t w4a16_grouped_workspace_size(int R, int E, const w4a8_wdesc* w);
  * packed, s_w, z: E stacked w4a8_pack_weights results (packed
  *          w4a8_packed_bytes(K, N) bytes each, s_w fp32 [E][G][N], z uint8
  *          [E][G][N], NULL iff symmetric), 16-byte aligned; w describes one.
- * Y        device bf16 [R][ldy], ldy >= N.
+ * Y        device bf16 [R][ldy], ldy >= N; overlaps no input.
  * workspace, ws_bytes: as for w8a8_grouped_gemm.
  * Limits: E <= 512, R <= 2^24, K <= 2^17.
  * Errors: INVALID_ARG, FORMAT_MISMATCH, UNSUPPORTED_SHAPE, WORKSPACE, CUDA;
@@ -547,7 +547,7 @@ W4A8_API size_t w4a8_moe_dispatch_workspace_size(int P, int E);
  * the grouped products.  expert_ids device int32 [P] in [0, E) (others are
  * reported as W4A8_ERR_INVALID_ARG through dev_status and taken as 0);
  * offsets_out int32 [E+1]; perm_out int32 [P]: position -> row; inv_out int32
- * [P]: row -> position.  E <= 512, P <= 2^26. */
+ * [P]: row -> position.  workspace: 16-byte aligned.  E <= 512, P <= 2^26. */
 W4A8_API w4a8_status w4a8_moe_dispatch(const int32_t* expert_ids, int P, int E, int32_t* offsets_out,
                                        int32_t* perm_out, int32_t* inv_out, void* workspace, size_t ws_bytes,
                                        int32_t* dev_status, void* stream);

@@ -476,9 +476,10 @@ def w8a8_pack_weights(W: torch.Tensor, status: Optional[torch.Tensor] = None, ou
         q = torch.empty(N, K, dtype=torch.int8, device=W.device)
         s = torch.empty(N, dtype=torch.float32, device=W.device)
     else:
-        e = int(expert)
+        e = -1 if expert is None else int(expert)
         if not 0 <= e < out.experts or (out.K, out.N) != (K, N):
             raise W4A8Error(1, "w8a8_pack_weights: no such slot in the stacked weight, or another shape")
+        _check_w8("w8a8_pack_weights", out, W.get_device())
         q, s = out.q_w[e], out.s_w[e]
     d = WDesc()
     _check(L.w8a8_pack_weights(_p(W), K, N, _p(q), _p(s), ctypes.byref(d), _p(status), _stream(W.device)),
@@ -490,6 +491,8 @@ def w8a8_pack_expert_weights(make_weight, E: int, K: int, N: int, device,
                              status: Optional[torch.Tensor] = None) -> PackedW8:
     """Quantizes E expert matrices (make_weight(e) -> fp32 [K, N] on `device`)
     into one stacked PackedW8."""
+    if E <= 0:
+        raise W4A8Error(1, "w8a8_pack_expert_weights: E must be positive")
     pw = PackedW8(q_w=torch.empty(E, N, K, dtype=torch.int8, device=device),
                   s_w=torch.empty(E, N, dtype=torch.float32, device=device),
                   desc=WDesc(8, 1, K, K, N, LAYOUT_VERSION), experts=E)
@@ -639,11 +642,11 @@ def w4a8_moe_dispatch(expert_ids: torch.Tensor, E: int, status: Optional[torch.T
     grouped products take them.  perm[position] = row, inv[row] = position."""
     L = load_library()
     where = "w4a8_moe_dispatch"
-    if not expert_ids.is_cuda or expert_ids.dtype.is_floating_point:
-        _refuse(where, "expert_ids must be integers on a CUDA device")
+    if not expert_ids.is_cuda:
+        _refuse(where, "expert_ids must be on a CUDA device")
     index, E = expert_ids.get_device(), int(E)
     _check_status(where, status, index)
-    ids = expert_ids.to(torch.int32).contiguous()
+    ids = _expert_ids(where, expert_ids, E)
     P = ids.numel()
     offsets = ids.new_empty(max(E + 1, 0))
     perm = ids.new_empty(P)
@@ -682,6 +685,15 @@ def _launch(index: int, where: str, fn, *args):
 
 def _refuse(where: str, what: str):
     raise W4A8Error(1, f"{where}: {what}")
+
+
+def _expert_ids(where: str, ids: torch.Tensor, E: int) -> torch.Tensor:
+    """Expert ids as contiguous int32; int64 ids outside [0, E) stay outside instead of wrapping into it."""
+    if ids.dtype == torch.int64:
+        ids = ids.clamp(-1, max(E, 0))
+    elif ids.dtype not in (torch.int32, torch.int16, torch.int8, torch.uint8):
+        _refuse(where, f"expert_ids must be integers, not {ids.dtype}")
+    return ids.to(torch.int32).contiguous()
 
 
 def _scratch(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor):
@@ -726,10 +738,15 @@ def _check_grouped(where: str, x, dtype, offsets, w, out, status):
             _refuse(where, "out must be bf16 [R, N] with unit column stride on the rows' device")
     if status is not None:
         _check_status(where, status, index)
-    return index, R, x.stride(0) if R > 1 else K, out, pitch
+    x_pitch = x.stride(0) if R > 1 else K
+    if (x_pitch | pitch) >> 31:
+        _refuse(where, "row strides must be below 2^31")
+    return index, R, x_pitch, out, pitch
 
 
 def _check_w8(where: str, w: PackedW8, index: int):
+    if not isinstance(w, PackedW8):
+        _refuse(where, "takes INT8 expert weights (PackedW8)")
     q, s, d, E = w.q_w, w.s_w, w.desc, w.experts
     N = d.N
     if q.dtype != torch.int8 or q.shape != (E, N, d.K) or not q.is_contiguous() or q.get_device() != index:
@@ -799,6 +816,8 @@ def w4a16_grouped_gemm(X: torch.Tensor, offsets: torch.Tensor, w: PackedWeight, 
     L = load_library()
     where = "w4a16_grouped_gemm"
     index, R, pitch, out, ldy = _check_grouped(where, X, torch.bfloat16, offsets, w, out, status)
+    if not isinstance(w, PackedWeight):
+        _refuse(where, "takes packed 4-bit expert weights (PackedWeight)")
     E, d, packed, s_w, z = w.experts, w.desc, w.packed, w.s_w, w.z
     K, N, group = d.K, d.N, d.group
     groups = (E, K // group if group > 0 else 0, N)
@@ -872,14 +891,14 @@ def w8a8_moe_experts(X: torch.Tensor, expert_ids: torch.Tensor, w1: PackedW8, w2
     index = X.get_device()
     R, H = X.shape
     E = w1.experts
-    if expert_ids.get_device() != index or expert_ids.numel() != R or expert_ids.dtype.is_floating_point:
+    if expert_ids.get_device() != index or expert_ids.numel() != R:
         _refuse(where, "expert_ids must be R integers on the rows' device")
     if E <= 0 or w2.experts != E or w1.desc.K != H:
         _refuse(where, "w1 and w2 must stack the same experts for H")
     _check_w8(where, w1, index)
     _check_w8(where, w2, index)
     _check_status(where, status, index)
-    X, ids = X.contiguous(), expert_ids.to(torch.int32).contiguous()
+    X, ids = X.contiguous(), _expert_ids(where, expert_ids, E)
     if out is None:
         out = X.new_empty((R, H))
     elif (out.dtype != torch.bfloat16 or out.shape != (R, H) or not out.is_contiguous()

@@ -126,7 +126,7 @@ __device__ __forceinline__ void build_group_table(const GroupTable& g, const int
                                                   int32_t* status) {
     const int tid = threadIdx.x, nthr = blockDim.x;
     for (int e = tid; e < E; e += nthr) {
-        const int32_t o0 = offsets[e], o1 = offsets[e + 1];
+        const int32_t o0 = __ldcg(offsets + e), o1 = __ldcg(offsets + e + 1);
         if ((o0 < 0) | (o1 > R) | (o1 < o0)) report_status(status, 1);
         const int32_t a = min(max(o0, 0), R), b = min(max(o1, 0), R);
         const int32_t c = max(b - a, 0);
@@ -504,9 +504,9 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
                         float y = sx * (sw0 * (float)(int32_t)a[j]);
                         if constexpr (GATEUP) {
                             const float up = sx * (sw1 * (float)(int32_t)b[j]);
-                            // the bf16 rounding of h is 2^-9: __expf and the fast quotient are within 2^-20
-                            // for |y| < 88 and give 0 below; with the exact ones this epilogue, not the
-                            // MMAs, set the pace (13,000 of 15,000 cycles a tile at K = 2048)
+                            // h's bf16 rounding is 2^-8: __expf and the fast quotient are within 2^-16 for
+                            // y > -87 and give 0 below, where silu is under 2e-36; with the exact ones this
+                            // epilogue, not the MMAs, set the pace (13,000 of 15,000 cycles a tile at K = 2048)
                             y = __fdividef(y, 1.0f + __expf(-y)) * up;
                         }
                         stg[j * 32 + lane] = f32_to_bf16_bits(y);

@@ -1474,7 +1474,8 @@ w4a8_status w4a8_moe_dispatch(const int32_t* expert_ids, int P, int E, int32_t* 
         return cudaMemsetAsync(offsets_out, 0, sizeof(int32_t) * (size_t)(E + 1), s) == cudaSuccess ? W4A8_OK
                                                                                                   : W4A8_ERR_CUDA;
     if (!expert_ids || !perm_out || !inv_out) return W4A8_ERR_INVALID_ARG;
-    if (!workspace || ws_bytes < w4a8_moe_dispatch_workspace_size(P, E)) return W4A8_ERR_WORKSPACE;
+    if (!workspace || ws_bytes < w4a8_moe_dispatch_workspace_size(P, E) || !aligned16(workspace))
+        return W4A8_ERR_WORKSPACE;
     int32_t* idx = static_cast<int32_t*>(workspace);
     float* wts = reinterpret_cast<float*>(idx + P);
     int32_t* mtile_off = reinterpret_cast<int32_t*>(wts + P);

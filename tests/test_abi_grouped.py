@@ -103,7 +103,7 @@ def test_dispatch_refusals(lib):
     call = lambda ids=FAKE, P=8, E=4, o=FAKE, ws=FAKE, wsb=BIG: lib.w4a8_moe_dispatch(  # noqa: E731
         ids, P, E, o, FAKE, FAKE, ws, wsb, None, None)
     assert call(ids=None) == 1 and call(P=-1) == 1 and call(E=0) == 1 and call(E=513) == 2 and call(o=None) == 1
-    assert call(ws=None) == 7 and call(wsb=16) == 7
+    assert call(ws=None) == 7 and call(wsb=16) == 7 and call(ws=ODD) == 7
 
 
 def test_binding_refusals():

@@ -85,13 +85,18 @@ def test_layer(m, T, E, topk, H, I, zipf):
     assert rel_rms(got, ref) <= 1e-2
 
 
-@pytest.mark.parametrize("R,E,I", [(1, 3, 128), (40, 3, 256), (130, 2, 384), (600, 4, 128)])
+@pytest.mark.parametrize("R,E,I", [
+    (1, 3, 128), (40, 3, 256), (130, 2, 384), (600, 4, 128),
+    (4, 1, 1024), (30, 1, 1152), (60, 1, 1280), (1200, 4, 1664),      # split along k, tiles of 16 to 128 rows
+])
 def test_gate_up_stage(m, R, E, I):
     """w2 = the identity in codes of 127 and scales of 1/127, so that a row
     comes out as its quantized h: y = s_h q_h / 127 * 127.  The INT8 code of h
     is at most half a step (s_h = max|h| / 127) off, the fp32 products
-    2^-22 of it, y one bf16 rounding; h itself was rounded to bf16 once and
-    its fp32 value is within 2^-20 (expf, a quotient and three products)."""
+    2^-22 of it, y one bf16 rounding; h itself was rounded to bf16 once (and
+    with it max|h|: 2^-8 of the half step).  Its fp32 value is within 2^-16
+    (__expf's error grows with its argument: 2 + 1.2 |x| units of 2^-23, |x| <
+    87): the rest of the half step's 2^-7, max|h| 2^-8 / 254, covers that."""
     layer = Layer(m, E, I, I, seed=R + I)
     layer.w2.q_w.zero_()
     layer.w2.q_w[:, torch.arange(I), torch.arange(I)] = 127
@@ -130,7 +135,7 @@ def test_experts_equal_layer_rows(m):
 def test_grouped_products_compose_to_the_layer(m):
     """The pieces as a user strings them together: route, dispatch, gather,
     grouped gate_up, silu * up, grouped down, combine.  gate_up leaves as bf16
-    here and stays fp32 in the layer (one more rounding of 2^-9 of each)."""
+    here and stays fp32 in the layer (one more rounding of 2^-8 of each)."""
     T, E, topk, H, I = 150, 8, 2, 512, 256
     layer = Layer(m, E, H, I, seed=3)
     inp = gen_moe_activations(T, H, E, seed=3)
@@ -152,9 +157,10 @@ def test_bad_ids_and_values_are_reported(m):
     st = m.new_status("cuda")
     m.w8a8_moe_experts(X, torch.tensor([0, 1, 2, 3, 4, -1]).cuda(), layer.w1, layer.w2, status=st)
     assert m.w4a8_get_device_status(st) == 1
-    st = m.new_status("cuda")
-    m.w4a8_moe_dispatch(torch.tensor([0, 9]).cuda(), 4, status=st)
-    assert m.w4a8_get_device_status(st) == 1
+    for ids in ([0, 9], [0, 2 ** 32], [-2 ** 40, 1]):
+        st = m.new_status("cuda")
+        m.w4a8_moe_dispatch(torch.tensor(ids).cuda(), 4, status=st)
+        assert m.w4a8_get_device_status(st) == 1
     logits = torch.randn(6, 4).cuda()
     for bad in ("x", "logits"):
         Xb, Lb = X.clone(), logits.clone()
@@ -162,6 +168,23 @@ def test_bad_ids_and_values_are_reported(m):
         st = m.new_status("cuda")
         m.w8a8_moe_grouped_gemm(Xb, Lb, 2, layer.w1, layer.w2, status=st)
         assert m.w4a8_get_device_status(st) == 4
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_two_streams_with_their_own_workspaces(m, T):
+    layer = Layer(m, 8, 256, 128, seed=4)
+    inp = gen_moe_activations(T, 256, 8, seed=1)
+    X, logits = inp.X.cuda(), inp.logits.cuda()
+    want = m.w8a8_moe_grouped_gemm(X, logits, 2, layer.w1, layer.w2)["out"]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(20):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(m.w8a8_moe_grouped_gemm(X, logits, 2, layer.w1, layer.w2)["out"])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got)
 
 
 def test_layer_captured(m):

@@ -67,6 +67,15 @@ CASES = [
     ([3] * 150, 128, 64, 128, True, 0, 0),
     ([1, 0, 40], 7168, 128, 64, False, 0, 0),               # long k
     ([24, 0, 1], 4096, 64, 128, True, 0, 0),
+    ([30], 1024, 64, 128, True, 0, 0),
+    ([30], 1088, 64, 64, False, 1, 0),
+    # 128-row tiles with every number of activation boxes, whole and split along k
+    ([1] * 26 + [60, 70, 40, 7], 256, 640, 128, True, 0, 3),
+    ([1] * 26 + [60, 70, 40, 7], 768, 640, 64, False, 0, 0),
+    # and 192-row tiles
+    ([193, 0, 192, 191, 97, 96, 65, 64, 33, 32, 1, 500, 10, 128, 2, 31], 320, 1280, 64, False, 2, 0),
+    ([193, 0, 192, 191, 97, 96, 65, 64, 33, 32, 1, 500, 10, 128, 2, 31], 1024, 1280, 128, True, 0, 0),
+    ([10] * 16, 896, 1280, 128, False, 0, 0),
 ]
 
 
@@ -206,11 +215,42 @@ def test_captured_with_changing_offsets(m):
         assert torch.equal(out, want)
 
 
+def test_two_streams_with_their_own_workspaces(m):
+    w, _ = _weights(m, 8, 1024, 256, 128, True, seed=10)
+    X = torch.randn(8, 1024, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    off = _offsets([1] * 8)
+    want = m.w4a16_grouped_gemm(X, off, w)
+    assert m.w4a16_grouped_workspace_size(8, w) > 0
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(30):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(m.w4a16_grouped_gemm(X, off, w))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got)
+
+
+def test_more_than_2_31_elements(m):
+    """Offsets into Y that pass 32 bits: rows at both ends against small calls."""
+    R, K, N = (1 << 17) + 5, 64, 16448
+    w, _ = _weights(m, 2, K, N, 64, True, seed=12)
+    X = torch.randn(R, K, device="cuda").bfloat16()
+    Y = m.w4a16_grouped_gemm(X, _offsets([9, R - 9]), w)
+    assert R * N > 2 ** 31
+    for e, rows in ((0, slice(0, 9)), (1, slice(9, 200)), (1, slice(R - 300, R))):   # K = 64: one sum, one order
+        n = rows.stop - rows.start
+        assert torch.equal(Y[rows], m.w4a16_grouped_gemm(X[rows].contiguous(), _offsets([n, 0] if e == 0 else [0, n]), w))
+
+
 def test_experts_of_a_layer(m):
     """Route, dispatch, gather, gate_up, silu * up, down, combine with the
     packed weights a W4A8 layer uses; against the same steps in fp64 on the
-    dequantized weights (bf16 roundings of gate_up, h and the expert rows:
-    2^-9 of each value and a few times that in the sums)."""
+    dequantized weights.  bf16 roundings, each at most 2^-8 of its value and
+    independent of the others: gate and up (h moves by at most twice that), h,
+    the expert rows; the fp32 sums and the last rounding are covered by their
+    root mean squares being at most 2^-8 / sqrt(3)."""
     T, E, topk, H, I, group = 40, 6, 2, 512, 256, 128
     w1, W1 = _weights(m, E, H, 2 * I, group, True, seed=1)
     w2, W2 = _weights(m, E, I, H, group, True, seed=2)

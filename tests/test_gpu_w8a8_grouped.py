@@ -53,6 +53,16 @@ CASES = [
     ([1] * 512, 128, 32, 0, 0),                        # the most experts
     ([5, 0, 90], 7168, 144, 0, 0),                     # long k, few tiles: split with many parts
     ([300, 20, 0, 700], 1408, 2048, 0, 0),
+    # one wave of 128-column tiles (the first two) and more than one, split along k
+    ([4], 2048, 208, 0, 0),
+    ([60], 2048, 400, 0, 0),
+    ([1] * 20, 896, 2304, 0, 0),
+    ([10] * 20, 1024, 2048, 0, 0),
+    ([20] * 16, 1280, 2560, 0, 0),
+    ([40] * 10, 1664, 3840, 0, 0),
+    # and whole
+    ([10] * 20, 128, 2048, 0, 0),
+    ([300, 20, 0, 700], 256, 3840, 3, 1),              # BN = 128
 ]
 
 
@@ -206,6 +216,49 @@ def test_two_streams_with_their_own_workspaces(m):
     assert all(torch.equal(y, want) for y in got)
 
 
+@pytest.mark.parametrize("R,K,N", [((1 << 17) + 5, 128, 16400), ((1 << 17) + 5, 16512, 16)])
+def test_more_than_2_31_elements(m, R, K, N):
+    """Offsets into Y and into the rows that pass 32 bits."""
+    w = _weights(m, 2, K, N, seed=12)
+    q = torch.randint(-127, 128, (R, K), dtype=torch.int8, device="cuda")
+    sx = torch.rand(R, device="cuda") + 0.5
+    Y = m.w8a8_grouped_gemm(q, sx, _offsets([9, R - 9]), w)
+    assert R * max(K, N) > 2 ** 31
+    for e, rows in ((0, slice(0, 9)), (1, slice(9, 200)), (1, slice(R - 300, R))):
+        assert torch.equal(Y[rows], m.w8a8_gemm(q[rows].contiguous(), sx[rows].clone(), _one(w, e, m)))
+
+
+def test_offsets_from_the_kernel_before(m):
+    """Offsets and rows written on the stream just before the call, over and over."""
+    w = _weights(m, 6, 512, 256, seed=13)
+    g = torch.Generator().manual_seed(4)
+    X = torch.randn(64, 512, generator=g).bfloat16().cuda()
+    ids = [torch.randint(0, 6, (64,), generator=g).cuda() for _ in range(8)]
+    want = [m.w8a8_grouped_linear(X[p.long()].contiguous(), o, w) for o, p, _ in
+            (m.w4a8_moe_dispatch(i, 6) for i in ids)]
+    torch.cuda.synchronize()
+    off, rows = torch.zeros(7, dtype=torch.int32, device="cuda"), torch.zeros_like(X)
+    for _ in range(10):
+        for i, ref in zip(ids, want):
+            o, p, _ = m.w4a8_moe_dispatch(i, 6)
+            rows.copy_(X[p.long()])
+            off.copy_(o)
+            assert torch.equal(m.w8a8_grouped_linear(rows, off, w), ref)
+            off.zero_()
+
+
+def test_one_row_of_any_stride(m):
+    w = _weights(m, 2, 256, 64, seed=14)
+    X = torch.randn(3, 256, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    off = _offsets([0, 1])
+    want = m.w8a8_grouped_linear(X[:1].contiguous(), off, w)
+    out = torch.zeros(64, 2, dtype=torch.bfloat16, device="cuda").t()[:1]
+    with pytest.raises(m.W4A8Error):        # columns not adjacent
+        m.w8a8_grouped_linear(X[:1], off, w, out=out)
+    row = torch.as_strided(torch.zeros(64, dtype=torch.bfloat16, device="cuda"), (1, 64), (1, 1))
+    assert torch.equal(m.w8a8_grouped_linear(X[::2][:1], off, w, out=row), want) and torch.equal(row, want)
+
+
 def test_refusals_of_the_binding(m):
     w = _weights(m, 4, 256, 64, seed=11)
     q, sx, _ = m.w4a8_quant_act(torch.randn(8, 256).bfloat16().cuda())
@@ -231,5 +284,15 @@ def test_refusals_of_the_binding(m):
     refused(m.w8a8_linear, torch.randn(8, 256).bfloat16().cuda(), w)
     refused(m.w8a8_grouped_linear, torch.randn(8, 256).cuda(), off, w)
     refused(m.w8a8_pack_weights, torch.randn(256, 64).cuda(), out=w, expert=4)
+    refused(m.w8a8_pack_weights, torch.randn(256, 64).cuda(), out=w)
+    refused(m.w8a8_pack_weights, torch.randn(256, 64).cuda(), expert=0, out=m.PackedW8(
+        w.q_w.cpu(), w.s_w.cpu(), w.desc, 4))                            # slots on another device
+    refused(m.w8a8_pack_expert_weights, None, 0, 256, 64, "cuda")
+    p4 = m.w4a8_pack_expert_weights(lambda e: torch.randn(256, 64).cuda(), 4, 256, 64, 64, True, "cuda")
+    refused(m.w8a8_grouped_gemm, q, sx, off, p4)                         # 4-bit experts
+    refused(m.w4a16_grouped_gemm, torch.randn(8, 256).bfloat16().cuda(), off, w)
+    refused(m.w4a8_moe_dispatch, torch.zeros(4, device="cuda"), 4)
+    refused(m.w4a8_moe_dispatch, torch.zeros(4, dtype=torch.int32), 4)
+    refused(m.w4a8_moe_dispatch, torch.zeros(4, dtype=torch.bool, device="cuda"), 4)
     # no rows at all
     assert m.w8a8_grouped_gemm(q[:0], sx[:0], torch.zeros_like(off), w).shape == (0, 64)
