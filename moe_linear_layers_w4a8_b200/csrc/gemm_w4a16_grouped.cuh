@@ -17,21 +17,27 @@
 //     k-block), so they need neither shared memory nor a proxy fence; with A in
 //     shared memory the stores and the fence took 500 of a k-block's 2,400
 //     cycles (512 rows over 32 experts, K = 7168, N = 4096: 264 -> 245 us).
-//   * 16 warps dequantize, four teams of 4, k-blocks in turn, so that one team's
-//     waits and stores overlap the others' arithmetic.  A thread takes one
-//     column's 64 k of a k-block: one scale, two 16-byte code chunks.  It gives
-//     the stage of packed weights back as soon as the codes are in registers.
-//     (Six teams at 64 registers a thread: no faster.)
+//   * 8 warps dequantize, two teams of 4, units in turn, so that one team's
+//     waits and stores overlap the other's arithmetic.  A thread takes one
+//     column's 128 k and gives the stage of packed weights back as soon as the
+//     codes are in registers.  (16 warps with 64 k each: what an iteration
+//     spends beside the weights, 125 instructions to their 187, made it 222 us
+//     to 214; three and four teams: no faster, they hold the MMA warp up.)
+//   * Activations come in stages of their own, longer in k where the rows are
+//     few: two units of them on their way (the stages of the weights) left the
+//     pipeline without arithmetic at 180 us, these at 145.
 //   * The producers and the MMA warp run converged, one lane issuing: a lone
 //     lane moves every descriptor and address to uniform registers one by one,
 //     135 cycles for each MMA instead of 32, 300 for each copy (245 -> 224 us
 //     from the producers, 310 -> 270 from the MMAs).
-//   * Bound by the dequantization: about 22 instructions for 8 weights, 13 of
-//     them integer ones at half rate: 230 cycles of a k-block's 540 per CTA if
-//     nothing else ran (0.29 us at any number of rows, which is the time of the
-//     MMAs at 150).  A mask is an immediate and 2^23 a register; a second
-//     constant for the flipped bit cost each mask a move (424 -> 369 us, 24576
-//     rows over 64 experts, K = 2048, N = 2816).
+//   * Bound by the dequantization (22 instructions for 8 weights, 13 of them
+//     at half rate, 26 cycles measured alone) beside the MMA warp's waits and
+//     issue: a unit takes 1,030 cycles of a CTA, 560 + 690 of a team's two
+//     units' worth in arithmetic, 840 of the MMA warp's.  At 144 rows and more
+//     the activations' way from L2 takes as long (10 TB/s over the SMs).  A
+//     mask is an immediate and 2^23 a register; a second constant for the
+//     flipped bit cost each mask a move (424 -> 369 us, 24576 rows over 64
+//     experts, K = 2048, N = 2816).
 // Tried and taken out: a kernel on mma.sync whose lanes keep the weights they
 // dequantize; its fragment loads and group scales came to 1.5 instructions for
 // a weight more: 280 us.
@@ -68,37 +74,42 @@ struct W16GroupedParams {
 
 constexpr int kW16GEpiWarp0 = 3;       // after the two producers and the MMA warp
 constexpr int kW16GDqWarp0 = 8;        // a multiple of 4: a warp's TMEM lanes follow from its number
-constexpr int kW16GKSW = 2;            // k-blocks of 64 per stage of packed weights: those of one pair of teams
-constexpr int kW16GSmall = 32;         // rows of the small activation box
+constexpr int kW16GKSW = 2;            // k-blocks of 64 per stage of packed weights: a unit's
 
-// Rows of the large activation box (one k-block) of a tile of bn rows.
-__host__ __device__ constexpr int w4a16_grouped_xrows(int bn) { return bn == 192 ? 96 : bn; }
+// Activation boxes: 32 rows x 8 k-blocks (tiles of 16 rows: 16 x 4), 64 rows
+// x 4, or, for tiles of more than 64 rows, the rows below x 1.
+__host__ __device__ constexpr int w4a16_grouped_rows0(int bn) { return bn == 16 ? 16 : 32; }
+__host__ __device__ constexpr int w4a16_grouped_kb0(int bn) { return bn == 16 ? 4 : 8; }
+constexpr int kW16GRows1 = 64, kW16GKb1 = 4;
+__host__ __device__ constexpr int w4a16_grouped_xrows(int bn) { return bn == 192 ? 96 : 128; }
 
 template <int BN>
 struct W16GCfg {
-    static constexpr int XB = BN * 128;                    // one k-block of activations: BN rows x 64 k bf16
-    static constexpr int STAGE = 2 * XB;                   // activations of two k-blocks
-    static constexpr int NS = BN <= 128 ? 4 : 2;           // stages: the CTA's units in turn
-    // Pairs of teams of 4 dequantizing warps; a pair fills a stage.  At most NS: a pair that is P units ahead
-    // has seen unit - P - NS released, and a barrier's parity tells two uses of a stage apart, not three.
-    static constexpr int PAIRS = 2;
-    static constexpr int DQ_WARPS = 8 * PAIRS;
+    // A stage of activations: 8 k-blocks of 32 rows, 4 of 64, 2 of BN.  Few rows take long stages, so that enough
+    // of k is on its way whatever the tile.
+    static constexpr int XSTAGE = BN <= 128 ? 32768 : 2 * BN * 128;
+    static constexpr int NX = BN <= 128 ? 4 : 3;
+    static constexpr int NS = BN <= 128 ? 4 : 2;           // stages of dequantized weights: the CTA's units in turn
+    // Teams of 4 dequantizing warps, a unit each in turn.  At most NS: a team that is P units ahead has seen
+    // unit - P - NS released, and a barrier's parity tells two uses of a stage apart, not three.
+    static constexpr int TEAMS = 2;
+    static constexpr int DQ_WARPS = 4 * TEAMS;
     static constexpr int THREADS = 32 * (kW16GDqWarp0 + DQ_WARPS);
-    static_assert(PAIRS <= NS, "a pair's lead");
-    static constexpr int XROWS = w4a16_grouped_xrows(BN);  // rows of the large activation box
+    static_assert(TEAMS <= NS, "a team's lead");
+    static constexpr int XROWS = w4a16_grouped_xrows(BN);  // rows of the largest activation box
     static constexpr int KSW = kW16GKSW;
     static constexpr int PK_HALF = KSW * 2048;             // codes of one 64-column half
     static constexpr int W_S = 2 * PK_HALF;                // fp32 scales [KSW][128]
     static constexpr int W_Z = W_S + KSW * 512;            // zero-points [KSW][128]
     static constexpr int W_STAGE = W_Z + KSW * 128;
-    // Stages of packed weights, the CTA's units in turn.  A multiple of PAIRS: a stage's readers are always the same
-    // pair, which has seen its last use (copies of different stages may land out of order).
-    static constexpr int NW = 2 * PAIRS;
+    // Stages of packed weights, the CTA's units in turn.  A multiple of TEAMS: a stage's readers are always the same
+    // team, which has seen its last use (copies of different stages may land out of order).
+    static constexpr int NW = 2 * TEAMS;
     static constexpr int STG = 4 * 1024;                   // output staging: 16 tokens x 32 columns per warp
-    static constexpr int OFF_W = NS * STAGE;
+    static constexpr int OFF_W = NX * XSTAGE;
     static constexpr int OFF_Y = OFF_W + NW * W_STAGE;
     static constexpr int OFF_BAR = OFF_Y + STG;
-    static constexpr int NUM_BARS = 2 * NW + 2 * NS + 5;
+    static constexpr int NUM_BARS = 2 * NW + 2 * NS + 2 * NX + 5;
     static constexpr int OFF_TABLE = OFF_BAR + NUM_BARS * 8;
     static constexpr int TABLE = 3 * (kGroupedMaxExperts + 1) * 4;
     static constexpr int OFF_MISC = OFF_TABLE + TABLE;
@@ -112,6 +123,25 @@ struct W16GCfg {
     static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128 || BN == 192, "BN");
     static_assert(W_S % 128 == 0 && W_STAGE % 128 == 0, "TMA destinations");
     static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// The activation stages of a tile: units to a stage, and bytes from one k-block
+// to the next.
+template <int BN>
+struct XPlan {
+    int units, kstride;
+    __device__ __forceinline__ explicit XPlan(int rows) {
+        if (BN <= 32 || rows <= w4a16_grouped_rows0(BN)) {
+            units = w4a16_grouped_kb0(BN) / 2;
+            kstride = w4a16_grouped_rows0(BN) * 128;
+        } else if (BN <= 64 || rows <= kW16GRows1) {
+            units = kW16GKb1 / 2;
+            kstride = kW16GRows1 * 128;
+        } else {
+            units = 1;
+            kstride = BN * 128;
+        }
+    }
 };
 
 // Scale and zero-point of a column's group for dequant_word32: pairs for the
@@ -170,18 +200,19 @@ __device__ __forceinline__ void mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem
 
 template <int BN, bool SYM>
 __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
-    w4a16_grouped_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_xs,
-                         const __grid_constant__ CUtensorMap tmap_s, const __grid_constant__ CUtensorMap tmap_z,
-                         const W16GroupedParams p) {
+    w4a16_grouped_kernel(const __grid_constant__ CUtensorMap tmap_x0, const __grid_constant__ CUtensorMap tmap_x1,
+                         const __grid_constant__ CUtensorMap tmap_x2, const __grid_constant__ CUtensorMap tmap_s, const __grid_constant__ CUtensorMap tmap_z, const W16GroupedParams p) {
     using C = W16GCfg<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* w_full = bars;                   // [NW] codes, scales, zero-points landed
-    uint64_t* w_empty = w_full + C::NW;        // [NW] the 16 dequant warps read them
-    uint64_t* full = w_empty + C::NW;          // [NS] weights written by a team, activations landed
+    uint64_t* w_empty = w_full + C::NW;        // [NW] a team read them
+    uint64_t* full = w_empty + C::NW;          // [NS] dequantized weights written by a team
     uint64_t* empty = full + C::NS;            // [NS] their MMAs completed
-    uint64_t* acc_full = empty + C::NS;        // [2]
+    uint64_t* x_full = empty + C::NS;          // [NX] activations landed
+    uint64_t* x_empty = x_full + C::NX;        // [NX] their MMAs completed
+    uint64_t* acc_full = x_empty + C::NX;      // [2]
     uint64_t* acc_empty = acc_full + 2;        // [2]
     uint64_t* drain = acc_empty + 2;           // [1]
     GroupTable g;
@@ -198,11 +229,15 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
         pdl_launch_dependents();
         for (int i = 0; i < C::NW; ++i) {
             mbar_init(&w_full[i], 1);
-            mbar_init(&w_empty[i], 8);
+            mbar_init(&w_empty[i], 4);
         }
         for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&full[i], 8 + 1);
+            mbar_init(&full[i], 4);
             mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < C::NX; ++i) {
+            mbar_init(&x_full[i], 1);
+            mbar_init(&x_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
@@ -212,7 +247,7 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
         *abort_flag = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
-        prefetch_tmap(&tmap_x);
+        prefetch_tmap(&tmap_x0);
         prefetch_tmap(&tmap_s);
         if (!SYM) prefetch_tmap(&tmap_z);
     }
@@ -281,41 +316,51 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
     } else if (warp == 2) {
         // ------------------------------------------- producer: activations --
         const bool leader = elect_one();
-        uint32_t phases = 0u, used = 0u, seq = 0u;
+        Ring rx;
+        long long issued = 0;
         bool ok = true;
         while (ok && walk.next(tile, u0, u1)) {
             const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
-            // few rows: one or two small boxes per k-block instead of the large ones
-            const bool small = C::XROWS > kW16GSmall && gt.rows <= (BN >= 128 ? 2 : 1) * kW16GSmall;
-            const int per = small ? kW16GSmall : C::XROWS;
-            const int boxes = gt.rows > per ? 2 : 1;
-            const CUtensorMap* map = small ? &tmap_xs : &tmap_x;
-            for (int u = u0; u < u1; ++u, ++seq) {
-                const int kb = 2 * u, len = min(2, KB - kb);
-                const int slot = seq % C::NS;
-                ok = warp_wait_bounded(&empty[slot], ((phases >> slot) & 1u) ^ 1u, wc);
+            const XPlan<BN> x(gt.rows);
+            const int boxes = gt.rows > C::XROWS ? 2 : 1;
+            for (int u = u0; u < u1; u += x.units) {
+                const int kb = 2 * u;
+                ok = warp_wait_bounded(&x_empty[rx.idx], rx.phase ^ 1u, wc);
                 if (!ok) break;
                 if (leader) {
-                    uint8_t* st = smem + slot * C::STAGE;
-                    mbar_arrive_expect_tx(&full[slot], len * boxes * (per * 128));
-                    for (int i = 0; i < len; ++i, st += C::XB) {
-                        tma_load_3d(st, map, &full[slot], 0, gt.row0, kb + i);
-                        if (boxes == 2) tma_load_3d(st + per * 128, map, &full[slot], 0, gt.row0 + per, kb + i);
+                    uint8_t* st = smem + rx.idx * C::XSTAGE;
+                    uint64_t* bar = &x_full[rx.idx];
+                    // a box's k-blocks past the tile's last are loaded (zeros past K), not used
+                    if (BN <= 32 || x.units == w4a16_grouped_kb0(BN) / 2) {
+                        mbar_arrive_expect_tx(bar, w4a16_grouped_rows0(BN) * w4a16_grouped_kb0(BN) * 128);
+                        tma_load_3d(st, &tmap_x0, bar, 0, gt.row0, kb);
+                    } else if (BN <= 64 || x.units == kW16GKb1 / 2) {
+                        mbar_arrive_expect_tx(bar, kW16GRows1 * kW16GKb1 * 128);
+                        tma_load_3d(st, &tmap_x1, bar, 0, gt.row0, kb);
+                    } else {
+                        const int len = min(2, KB - kb);
+                        mbar_arrive_expect_tx(bar, len * boxes * (C::XROWS * 128));
+                        for (int i = 0; i < len; ++i, st += BN * 128) {
+                            tma_load_3d(st, &tmap_x2, bar, 0, gt.row0, kb + i);
+                            if (boxes == 2)
+                                tma_load_3d(st + C::XROWS * 128, &tmap_x2, bar, 0, gt.row0 + C::XROWS, kb + i);
+                        }
                     }
                 }
                 __syncwarp();
-                phases ^= 1u << slot;
-                used |= 1u << slot;
+                rx.next(C::NX);
+                ++issued;
             }
         }
-        // copies in flight land before the CTA leaves.  A stage completes with its weights; when the CTA gives
-        // up they may never come, and the wait runs to its limit.
+        // copies in flight land before the CTA leaves
         if (leader) {
             WaitCtx wd = wc;
             volatile int no_abort = 0;
             wd.abort = &no_abort;
-            for (int i = 0; i < C::NS; ++i)
-                if ((used >> i) & 1u) (void)wait_bounded(&full[i], ((phases >> i) & 1u) ^ 1u, wd);
+            for (long long k = 0; k < issued && k < C::NX; ++k) {
+                ring_back(rx, C::NX);
+                (void)wait_bounded(&x_full[rx.idx], rx.phase, wd);
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -325,7 +370,7 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
         // instead of being moved there one by one.
         {
             const bool leader = elect_one();
-            Ring rc;
+            Ring rc, rx;
             uint32_t phases = 0u, seq = 0u;
             bool ok = true;
             while (ok && walk.next(tile, u0, u1)) {
@@ -334,12 +379,16 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
                 if (!warp_wait_bounded(&acc_empty[rc.idx], rc.phase ^ 1u, wc)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + rc.idx * BN;
+                const XPlan<BN> x(gt.rows);
+                int xu = 0;                          // the unit's place in its activation stage
                 for (int u = u0; u < u1; ++u, ++seq) {
                     const int slot = seq % C::NS;
+                    if (xu == 0 && !warp_wait_bounded(&x_full[rx.idx], rx.phase, wc)) { ok = false; break; }
                     if (!warp_wait_bounded(&full[slot], (phases >> slot) & 1u, wc)) { ok = false; break; }
                     tc_fence_after();
+                    const bool last = xu == x.units - 1 || u == u1 - 1;
                     if (leader) {
-                        const uint32_t st = smem_u32(smem + slot * C::STAGE);
+                        const uint32_t st = smem_u32(smem + rx.idx * C::XSTAGE) + xu * 2 * x.kstride;
                         const uint32_t a = tmem_base + C::A_COL0 + slot * 64;
                         const uint64_t bdesc = umma_desc_kmajor(st, 128);
 #pragma unroll
@@ -348,12 +397,15 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
                         if (2 * u + 1 < KB) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_bf16_tmem_a(d_tmem, a + 32 + 8 * kk, bdesc + (C::XB >> 4) + 2 * kk, idesc, 1u);
+                                mma_bf16_tmem_a(d_tmem, a + 32 + 8 * kk, bdesc + (x.kstride >> 4) + 2 * kk, idesc, 1u);
                         }
                         tc_commit(&empty[slot]);
+                        if (last) tc_commit(&x_empty[rx.idx]);
                     }
                     __syncwarp();
                     phases ^= 1u << slot;
+                    xu = last ? 0 : xu + 1;
+                    if (last) rx.next(C::NX);
                 }
                 if (!ok) break;
                 if (leader) tc_commit(&acc_full[rc.idx]);
@@ -372,62 +424,71 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
         }
     } else if (warp >= kW16GDqWarp0) {
         // ----------------------------------------------------- dequantize --
-        // The teams take k-blocks in turn, so that one's waits and hand-over
-        // overlap the others' arithmetic.  A thread takes one column's 64 k:
-        // they lie in one group, so its scale is set up once for 64 weights.
+        // The teams take units in turn, so that one's waits and hand-over
+        // overlap the other's arithmetic.  A thread takes one column's 128 k.
         const int team = (warp - kW16GDqWarp0) >> 2;
         const int r = (warp & 3) * 32 + lane;            // weight column within the tile = A row = TMEM lane
         const int hf = r >> 6;
-        const uint32_t a_tmem = tmem_base + (((uint32_t)(warp & 3) * 32) << 16) + C::A_COL0 + (team & 1) * 32;
-        const int j = team & 1;                          // this team's k-block of its pair's two
-        const uint32_t off_c = hf * C::PK_HALF + j * 2048 + (r & 63) * 16;
-        const uint32_t off_s = C::W_S + ((j >> kb_shift) * 128 + r) * 4, off_z = C::W_Z + (j >> kb_shift) * 128 + r;
+        const uint32_t a_tmem = tmem_base + (((uint32_t)(warp & 3) * 32) << 16) + C::A_COL0;
+        const uint32_t off_c = hf * C::PK_HALF + (r & 63) * 16;
+        const int g1 = 1 >> kb_shift;                    // the second k-block's group row
         uint32_t seq = 0u;                               // units of this CTA so far
-        uint32_t own = team >> 1;                        // the pair's next among them: every C::PAIRS-th
+        uint32_t own = team;                             // the team's next among them: every TEAMS-th
         bool ok = true;
         while (ok && walk.next(tile, u0, u1)) {
             const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
             const bool valid = hf * 64 < min(128, p.N - gt.nt * 128);
             const uint32_t end = seq + (uint32_t)(u1 - u0);
-            for (; own < end; own += C::PAIRS) {
+            for (; own < end; own += C::TEAMS) {
                 const int u = u0 + (int)(own - seq);
                 const uint32_t slot = own % C::NW;
                 ok = warp_wait_bounded(&w_full[slot], (own / C::NW) & 1u, wc);
                 if (!ok) break;
-                // everything this thread needs of the stage, which is then free again
-                const bool mine = 2 * u + j < KB;        // warp-uniform
+                const bool two = 2 * u + 1 < KB;         // warp-uniform
                 const uint8_t* st = smem + C::OFF_W + slot * C::W_STAGE;
-                uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0;
-                float sv = 0.0f;                         // columns past N: scale 0
-                uint32_t zv = 0u;
-                if (valid && mine) {
-                    c0 = *reinterpret_cast<const uint4*>(st + off_c);
-                    c1 = *reinterpret_cast<const uint4*>(st + off_c + 1024);
-                    sv = *reinterpret_cast<const float*>(st + off_s);
-                    if (!SYM) zv = st[off_z];
+                // everything this thread needs of the stage, which is then free again
+                uint4 c[4] = {};                         // columns past N: scale 0
+                float s0 = 0.0f, s1 = 0.0f;
+                uint32_t z0 = 0u, z1 = 0u;
+                if (valid) {
+                    c[0] = *reinterpret_cast<const uint4*>(st + off_c);
+                    c[1] = *reinterpret_cast<const uint4*>(st + off_c + 1024);
+                    s0 = *reinterpret_cast<const float*>(st + C::W_S + r * 4);
+                    if (!SYM) z0 = st[C::W_Z + r];
+                    if (two) {
+                        c[2] = *reinterpret_cast<const uint4*>(st + off_c + 2048);
+                        c[3] = *reinterpret_cast<const uint4*>(st + off_c + 3072);
+                        s1 = *reinterpret_cast<const float*>(st + C::W_S + (g1 * 128 + r) * 4);
+                        if (!SYM) z1 = st[C::W_Z + g1 * 128 + r];
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&w_empty[slot]);
                 const uint32_t as = own % C::NS;
                 uint32_t out[16];                        // 32 k of the column, bf16 pairs in k order
                 NibblePairs<SYM> q;
-                q.set(sv, zv);
+                q.set(s0, z0);
                 auto chunk = [&](const uint4& c) {
                     dequant_word32<SYM>(c.x, q, out, out + 8);
                     dequant_word32<SYM>(c.y, q, out + 2, out + 10);
                     dequant_word32<SYM>(c.z, q, out + 4, out + 12);
                     dequant_word32<SYM>(c.w, q, out + 6, out + 14);
                 };
-                if (mine) chunk(c0);
+                chunk(c[0]);
                 ok = warp_wait_bounded(&empty[as], ((own / C::NS) & 1u) ^ 1u, wc);
                 if (!ok) break;
-                if (mine) {
-                    tc_fence_after();
-                    tmem_st32<16>(a_tmem + as * 64, out);
-                    chunk(c1);
-                    tmem_st32<16>(a_tmem + as * 64 + 16, out);
-                    tmem_wait_st();
+                tc_fence_after();
+                tmem_st32<16>(a_tmem + as * 64, out);
+                chunk(c[1]);
+                tmem_st32<16>(a_tmem + as * 64 + 16, out);
+                if (two) {
+                    if (kb_shift == 0) q.set(s1, z1);
+                    chunk(c[2]);
+                    tmem_st32<16>(a_tmem + as * 64 + 32, out);
+                    chunk(c[3]);
+                    tmem_st32<16>(a_tmem + as * 64 + 48, out);
                 }
+                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[as]);
@@ -543,11 +604,9 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
 }
 
 // Launches the grouped W4A16 tile kernel for a tile of BN in {16, 32, 64, 128,
-// 192} rows (defined in gemm_w4a16_grouped.cu).  tmap_xs: boxes of kW16GSmall
-// rows x one k-block.  Status codes as in w4a8.h.
-int launch_w4a16_grouped(int bn, bool sym, const CUtensorMap& tmap_x, const CUtensorMap& tmap_xs,
-                         const CUtensorMap& tmap_s, const CUtensorMap& tmap_z, const W16GroupedParams& p, int grid,
-                         cudaStream_t stream);
-
+// 192} rows (defined in gemm_w4a16_grouped.cu).  tmap_x: the three activation
+// boxes.  Status codes as in w4a8.h.
+int launch_w4a16_grouped(int bn, bool sym, const CUtensorMap (&tmap_x)[3], const CUtensorMap& tmap_s,
+                         const CUtensorMap& tmap_z, const W16GroupedParams& p, int grid, cudaStream_t stream);
 
 }  // namespace w4a8

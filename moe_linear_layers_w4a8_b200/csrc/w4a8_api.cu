@@ -777,9 +777,10 @@ w4a8_status launch_w16_grouped(const uint16_t* X, int ldx, const int32_t* offset
     const int bn = pl.bn, G = w->K / w->group;
     // scale / zero-point rows of one weight stage (a whole number of groups from its first k on)
     const int sg_rows = 64 * kW16GKSW / w->group;
-    CUtensorMap tx, txs, ts, tz;
-    if (!make_bf16_k64_tmap(&tx, X, R, w->K, ldx, w4a16_grouped_xrows(bn), 1) ||
-        !make_bf16_k64_tmap(&txs, X, R, w->K, ldx, kW16GSmall, 1) ||
+    CUtensorMap tx[3], ts, tz;
+    if (!make_bf16_k64_tmap(&tx[0], X, R, w->K, ldx, w4a16_grouped_rows0(bn), w4a16_grouped_kb0(bn)) ||
+        !make_bf16_k64_tmap(&tx[1], X, R, w->K, ldx, kW16GRows1, kW16GKb1) ||
+        !make_bf16_k64_tmap(&tx[2], X, R, w->K, ldx, w4a16_grouped_xrows(bn), 1) ||
         !make_group_tmap(&ts, s_w, E * G, w->N, true, sg_rows))
         return W4A8_ERR_CUDA;
     if (z) {
@@ -812,7 +813,7 @@ w4a8_status launch_w16_grouped(const uint16_t* X, int ldx, const int32_t* offset
     p.status = dev_status;
     p.wait_ns = kDefaultWaitNs;
     return static_cast<w4a8_status>(
-        launch_w4a16_grouped(bn, w->symmetric != 0, tx, txs, ts, tz, p, pl.grid, s));
+        launch_w4a16_grouped(bn, w->symmetric != 0, tx, ts, tz, p, pl.grid, s));
 }
 
 }  // namespace
