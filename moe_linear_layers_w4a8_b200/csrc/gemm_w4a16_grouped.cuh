@@ -76,10 +76,10 @@ constexpr int kW16GEpiWarp0 = 3;       // after the two producers and the MMA wa
 constexpr int kW16GDqWarp0 = 8;        // a multiple of 4: a warp's TMEM lanes follow from its number
 constexpr int kW16GKSW = 2;            // k-blocks of 64 per stage of packed weights: a unit's
 
-// Activation boxes: 32 rows x 8 k-blocks (tiles of 16 rows: 16 x 4), 64 rows
+// Activation boxes: 32 rows x 8 k-blocks (tiles of 16 rows: 16 x 2), 64 rows
 // x 4, or, for tiles of more than 64 rows, the rows below x 1.
 __host__ __device__ constexpr int w4a16_grouped_rows0(int bn) { return bn == 16 ? 16 : 32; }
-__host__ __device__ constexpr int w4a16_grouped_kb0(int bn) { return bn == 16 ? 4 : 8; }
+__host__ __device__ constexpr int w4a16_grouped_kb0(int bn) { return bn == 16 ? 2 : 8; }
 constexpr int kW16GRows1 = 64, kW16GKb1 = 4;
 __host__ __device__ constexpr int w4a16_grouped_xrows(int bn) { return bn == 192 ? 96 : 128; }
 

@@ -464,6 +464,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const float* __restrict
 // the prefix over experts of ceil(count / BN) m-tiles for the grouped GEMMs.
 // ---------------------------------------------------------------------------
 constexpr int kDispatchThreads = 256;
+constexpr int kDispatchOneCta = 512;   // tokens up to which one CTA is faster than three launches
 constexpr int kMaxExperts = 512;
 
 __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const int32_t* __restrict__ idx, int T,
@@ -546,31 +547,60 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const int32_
     }
 }
 
-// Routing and dispatch of a few tokens (T <= 16) in one CTA: a layer step of
-// single tokens is a chain of launches whose own work is short (routing and
-// dispatch as two launches: 4.0 + 5.8 us for one token of 64 experts, most of
-// it launch and the walk over the experts by one thread; this kernel: 5.0 us).
-// Each warp routes a token; a pair's rank among its expert's is counted over
-// the earlier pairs; the offsets are one warp's scan.  Same outputs as
-// route_topk_kernel and dispatch_kernel.
-constexpr int kRouteDispatchTokens = 16;
+// Routing, dispatch and quantization of a few tokens (T <= 16) in one launch,
+// a CTA for each token: a layer step of single tokens is a chain of launches
+// whose own work is short (one token of 64 experts: 4.0 + 5.8 us for routing
+// and dispatch, 3 for the quantization).  Every CTA routes all tokens, a warp
+// each; a pair's rank among its expert's is counted over the earlier pairs;
+// the offsets are one warp's scan.  Then the CTA quantizes its token's row,
+// loaded meanwhile, into its positions.  Same outputs as route_topk_kernel,
+// dispatch_kernel and quant_act_kernel; K <= 8192.
+constexpr int kRouteQuantTokens = 16;
+constexpr int kRouteQuantThreads = 32 * kRouteQuantTokens;
 
 template <int EPL>
-__global__ void __launch_bounds__(32 * kRouteDispatchTokens) route_dispatch_kernel(
+__global__ void __launch_bounds__(kRouteQuantThreads) route_quant_kernel(
     const float* __restrict__ logits, int T, int E, int topk, int32_t* __restrict__ idx, float* __restrict__ p,
-    int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ inv, int32_t* status) {
+    int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ inv,
+    const uint16_t* __restrict__ X, int K, int8_t* __restrict__ q, float* __restrict__ s_x, int32_t* status) {
+    constexpr int kPairs = kRouteQuantTokens * 16;
     __shared__ int32_t first[kMaxExperts];                         // counts, then first positions
-    __shared__ int32_t expert[kRouteDispatchTokens * 16];          // of every pair
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int32_t expert[kPairs];
+    __shared__ float weight[kPairs];
+    __shared__ int32_t place[16];                                  // positions of this CTA's token
+    __shared__ uint32_t red_max[kRouteQuantThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = blockIdx.x;
+    const bool one = t == 0;                                       // writes what is common
     pdl_launch_dependents();
-    for (int e = tid; e < E; e += blockDim.x) first[e] = 0;
-    if (warp < T) route_token<EPL>(logits, warp, E, topk, idx, p, status);
+    const int nchunk = K >> 3;
+    const uint4* xr = reinterpret_cast<const uint4*>(X + (size_t)t * K);
+    uint4 raw[2];
+    uint32_t am2 = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = i * kRouteQuantThreads + tid;
+        raw[i] = c < nchunk ? __ldg(xr + c) : make_uint4(0, 0, 0, 0);
+    }
+    for (int e = tid; e < E; e += kRouteQuantThreads) first[e] = 0;
+    if (warp < T) route_token<EPL>(logits, warp, E, topk, expert, weight, one ? status : nullptr);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        am2 = absmax_bf16x2(am2, raw[i].x);
+        am2 = absmax_bf16x2(am2, raw[i].y);
+        am2 = absmax_bf16x2(am2, raw[i].z);
+        am2 = absmax_bf16x2(am2, raw[i].w);
+    }
+    uint32_t am = __reduce_max_sync(0xFFFFFFFFu, max(am2 & 0xFFFFu, am2 >> 16));
+    if (lane == 0) red_max[warp] = am;
     __syncthreads();
     const int pairs = T * topk;                                    // at most 256
     int e = 0;
     if (tid < pairs) {
-        e = idx[tid];
-        expert[tid] = e;
+        e = expert[tid];
+        if (one) {
+            idx[tid] = e;
+            p[tid] = weight[tid];
+        }
         atomicAdd(&first[e], 1);
     }
     __syncthreads();
@@ -588,18 +618,40 @@ __global__ void __launch_bounds__(32 * kRouteDispatchTokens) route_dispatch_kern
         for (int k = e0; k < e1; ++k) {
             const int32_t c = first[k];
             first[k] = run;
-            offsets[k] = run;
+            if (one) offsets[k] = run;
             run += c;
         }
-        if (lane == 31) offsets[E] = pairs;
+        if (one && lane == 31) offsets[E] = pairs;
     }
     __syncthreads();
     if (tid < pairs) {
         int32_t pos = first[e];
         for (int k = 0; k < tid; ++k) pos += expert[k] == e;
-        inv[tid] = pos;
-        perm[pos] = tid;
+        if (one) {
+            inv[tid] = pos;
+            perm[pos] = tid;
+        }
+        const int j = tid - t * topk;
+        if (j >= 0 && j < topk) place[j] = pos;
     }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRouteQuantThreads / 32; ++i) am = max(am, red_max[i]);
+    const float s = __fdiv_rn(bf16_bits_to_f32(am), 127.0f);
+    const float d = (s > 0.0f) ? s : 1.0f;
+    const float r_d = __frcp_rn(d);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = i * kRouteQuantThreads + tid;
+        if (c < nchunk) {
+            uint32_t packed[2];
+            quant_chunk8(raw[i], d, r_d, packed[0], packed[1], nullptr);
+            for (int j = 0; j < topk; ++j)
+                *reinterpret_cast<uint2*>(q + (size_t)place[j] * K + (size_t)c * 8) = make_uint2(packed[0], packed[1]);
+        }
+    }
+    if (tid < topk) s_x[place[tid]] = s;
+    if (tid == 0 && am >= 0x7F80u) report_status(status, kStatusNonfinite);  // an Inf or NaN in the row
 }
 
 // The same dispatch spread over many CTAs, for many tokens: each CTA owns a
@@ -716,8 +768,11 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_scatter_kernel(cons
 // ---------------------------------------------------------------------------
 // Weighted combine ("Kimi 2.7 MoE, 4-bit storage to INT8" §4.3-4.4 step 5):
 // out[t] = sum_j p[t,j] * y[inv(t,j)], fp32 in slot order, one bf16 rounding.
-// One thread per (token, 8 consecutive columns): 16-byte loads and stores.
+// One thread per (token, 8 consecutive columns): 16-byte loads and stores.  B
+// slots are loaded together: 8 for few tokens (latency: 5.0 -> 4.1 us for 333
+// x 1152), 4 for many (occupancy: 24.0 us to 26.8 for 4096 x 2048).
 // ---------------------------------------------------------------------------
+template <int B>
 __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ Yd,
                                                       const float* __restrict__ p,
                                                       const int32_t* __restrict__ inv, int T, int topk, int H,
@@ -726,21 +781,41 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
     const int cpr = H >> 3;
     const long long gid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (gid >= (long long)T * cpr) return;
-    const int t = (int)(gid / cpr), c = (int)(gid % cpr);
+    int t, c;
+    if ((gid >> 32) == 0) {  // a 64-bit division takes about as long as a load
+        t = (int)((uint32_t)gid / (uint32_t)cpr);
+        c = (int)((uint32_t)gid % (uint32_t)cpr);
+    } else {
+        t = (int)(gid / cpr);
+        c = (int)(gid % cpr);
+    }
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-    for (int j = 0; j < topk; ++j) {
-        // inv == null: the rows are already in (token, slot) order
-        const int r = inv ? __ldg(inv + (size_t)t * topk + j) : t * topk + j;
-        const float w = __ldg(p + (size_t)t * topk + j);
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(Yd + (size_t)r * H) + c);
-        const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+    // B slots at a time: their positions, then their rows, each in one round trip
+    for (int j0 = 0; j0 < topk; j0 += B) {
+        int r[B];
+        float w[B];
+        uint4 v[B];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t bits = (e & 1) ? (ws[e >> 1] >> 16) : (ws[e >> 1] & 0xFFFFu);
-            acc[e] = fmaf(w, bf16_bits_to_f32(bits), acc[e]);
+        for (int i = 0; i < B; ++i) {
+            const size_t at = (size_t)t * topk + min(j0 + i, topk - 1);
+            // inv == null: the rows are already in (token, slot) order
+            r[i] = inv ? __ldg(inv + at) : (int)at;
+            w[i] = __ldg(p + at);
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (j0 + i < topk) v[i] = __ldg(reinterpret_cast<const uint4*>(Yd + (size_t)r[i] * H) + c);
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            if (j0 + i >= topk) break;
+            const uint32_t ws[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t bits = (e & 1) ? (ws[e >> 1] >> 16) : (ws[e >> 1] & 0xFFFFu);
+                acc[e] = fmaf(w[i], bf16_bits_to_f32(bits), acc[e]);
+            }
         }
     }
     uint32_t o[4];

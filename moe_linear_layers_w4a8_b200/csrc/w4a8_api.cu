@@ -353,11 +353,12 @@ w4a8_status launch_route(const float* logits, int T, int E, int topk, int32_t* i
     return last_cuda();
 }
 
-// Routing and dispatch of T <= kRouteDispatchTokens tokens in one launch.
-w4a8_status launch_route_dispatch(const float* logits, int T, int E, int topk, int32_t* idx, float* w,
-                                  int32_t* offsets, int32_t* perm, int32_t* inv, int32_t* status, cudaStream_t s) {
+// Routing, dispatch and quantization of T <= kRouteQuantTokens tokens in one launch.
+w4a8_status launch_route_quant(const float* logits, int T, int E, int topk, int32_t* idx, float* w, int32_t* offsets,
+                               int32_t* perm, int32_t* inv, const uint16_t* X, int K, int8_t* q, float* s_x,
+                               int32_t* status, cudaStream_t s) {
     switch ((E + 31) / 32) {
-#define W4A8_ROUTE(n) case n: route_dispatch_kernel<n><<<1, 32 * kRouteDispatchTokens, 0, s>>>(logits, T, E, topk, idx, w, offsets, perm, inv, status); break;
+#define W4A8_ROUTE(n) case n: route_quant_kernel<n><<<(unsigned)T, kRouteQuantThreads, 0, s>>>(logits, T, E, topk, idx, w, offsets, perm, inv, X, K, q, s_x, status); break;
         W4A8_ROUTE(1) W4A8_ROUTE(2) W4A8_ROUTE(3) W4A8_ROUTE(4) W4A8_ROUTE(5) W4A8_ROUTE(6) W4A8_ROUTE(7)
         W4A8_ROUTE(8) W4A8_ROUTE(9) W4A8_ROUTE(10) W4A8_ROUTE(11) W4A8_ROUTE(12) W4A8_ROUTE(13)
         W4A8_ROUTE(14) W4A8_ROUTE(15) W4A8_ROUTE(16)
@@ -373,7 +374,7 @@ w4a8_status launch_route_dispatch(const float* logits, int T, int E, int topk, i
 w4a8_status launch_dispatch(const int32_t* idx, int T, int E, int topk, int bn, int32_t* offsets, int32_t* mtile_off,
                             int32_t* perm, int32_t* inv, int32_t* dcnt, cudaStream_t s, bool pdl = false) {
     w4a8_status st;
-    if (T <= kDispatchThreads) {
+    if (T <= kDispatchOneCta) {
         st = launch_maybe_pdl(dispatch_kernel, 1, kDispatchThreads, s, pdl, idx, T, E, topk, bn, offsets, mtile_off,
                               perm, inv);
         return st != W4A8_OK ? st : last_cuda();
@@ -385,6 +386,16 @@ w4a8_status launch_dispatch(const int32_t* idx, int T, int E, int topk, int bn, 
     if (st != W4A8_OK || (st = last_cuda()) != W4A8_OK) return st;
     st = launch_maybe_pdl(dispatch_scatter_kernel, (unsigned)C, kDispatchThreads, s, pdl, idx, T, E, topk, tpc, dcnt,
                           perm, inv);
+    return st != W4A8_OK ? st : last_cuda();
+}
+
+// The weighted sum of a token's rows; inv == null: rows in (token, slot) order.
+w4a8_status launch_combine(const uint16_t* y, const float* w, const int32_t* inv, int T, int topk, int H, uint16_t* out,
+                           cudaStream_t s, bool pdl = false) {
+    const unsigned blocks = (unsigned)(((long long)T * (H / 8) + 255) / 256);
+    const w4a8_status st =
+        blocks <= 512 ? launch_maybe_pdl(combine_kernel<8>, blocks, 256, s, pdl, y, w, inv, T, topk, H, out)
+                      : launch_maybe_pdl(combine_kernel<4>, blocks, 256, s, pdl, y, w, inv, T, topk, H, out);
     return st != W4A8_OK ? st : last_cuda();
 }
 
@@ -1108,11 +1119,7 @@ w4a8_status moe_impl(const uint16_t* X, const float* logits, int T, int E, int t
     }
     // 7. weighted combine
     if (!mark(6)) return W4A8_ERR_CUDA;
-    {
-        const long long n = (long long)T * (H / 8);
-        combine_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(yd, topk_w_out, inv, T, topk, H, out);
-        if ((st = last_cuda()) != W4A8_OK) return st;
-    }
+    if ((st = launch_combine(yd, topk_w_out, inv, T, topk, H, out, s)) != W4A8_OK) return st;
     if (!mark(7)) return W4A8_ERR_CUDA;
     return W4A8_OK;
 }
@@ -1194,10 +1201,7 @@ w4a8_status w4a8_moe_combine(const uint16_t* y_rows, const float* topk_w, int T,
     if (T < 0 || topk <= 0 || H <= 0 || H % 8 != 0) return W4A8_ERR_INVALID_ARG;
     if (T == 0) return W4A8_OK;
     if (!y_rows || !topk_w || !out || !aligned16(y_rows) || !aligned16(out)) return W4A8_ERR_INVALID_ARG;
-    const long long n = (long long)T * (H / 8);
-    combine_kernel<<<(unsigned)((n + 255) / 256), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        y_rows, topk_w, nullptr, T, topk, H, out);
-    return last_cuda();
+    return launch_combine(y_rows, topk_w, nullptr, T, topk, H, out, static_cast<cudaStream_t>(stream));
 }
 
 w4a8_status w4a8_get_device_status(const int32_t* dev_status, void* stream) {
@@ -1378,9 +1382,12 @@ w4a8_status moe_w8_impl(const uint16_t* X, const float* logits, const int32_t* p
     uint16_t* yd = reinterpret_cast<uint16_t*>(ws + L.base.yd);
     w4a8_status st;
     int32_t* perm = reinterpret_cast<int32_t*>(ws + L.base.perm);
-    if (!pre_ids && T <= kRouteDispatchTokens) {
-        if ((st = launch_route_dispatch(logits, T, E, topk, idx, wts, offsets, perm, inv, dev_status, s)) != W4A8_OK)
-            return st;
+    // Every kernel waits for the one before it inside (programmatic
+    // stream serialization), so that a launch's start-up overlaps that one's end.
+    const bool fused = !pre_ids && T <= kRouteQuantTokens;
+    if (fused) {
+        st = launch_route_quant(logits, T, E, topk, idx, wts, offsets, perm, inv, X, H, qx, sx, dev_status, s);
+        if (st != W4A8_OK) return st;
     } else {
         if (pre_ids) {
             preroute_kernel<<<(unsigned)((T + 255) / 256), 256, 0, s>>>(pre_ids, T, E, idx, wts, dev_status);
@@ -1392,18 +1399,15 @@ w4a8_status moe_w8_impl(const uint16_t* X, const float* logits, const int32_t* p
         st = launch_dispatch(idx, T, E, topk, 128, offsets, reinterpret_cast<int32_t*>(ws + L.base.mtile_off), perm, inv,
                              reinterpret_cast<int32_t*>(ws + L.base.dcnt), s, true);
         if (st != W4A8_OK) return st;
+        if ((st = launch_quant(X, T, H, H, qx, sx, nullptr, 0, inv, topk, dev_status, s, true)) != W4A8_OK) return st;
     }
-    // Every kernel waits for the one before it inside (programmatic
-    // stream serialization), so that a launch's start-up overlaps that one's end.
-    if ((st = launch_quant(X, T, H, H, qx, sx, nullptr, 0, inv, topk, dev_status, s, true)) != W4A8_OK) return st;
-    st = launch_w8_grouped(qx, sx, offsets, R, E, w1_q, w1_s, I, H, true, h, I, ws + L.split, dev_status, s, true);
+    // the fused kernel writes the offsets after it lets its dependents start
+    st = launch_w8_grouped(qx, sx, offsets, R, E, w1_q, w1_s, I, H, true, h, I, ws + L.split, dev_status, s, !fused);
     if (st != W4A8_OK) return st;
     if ((st = launch_quant(h, R, I, I, qh, sh, nullptr, 0, nullptr, 0, dev_status, s, true)) != W4A8_OK) return st;
     st = launch_w8_grouped(qh, sh, offsets, R, E, w2_q, w2_s, H, I, false, yd, H, ws + L.split, dev_status, s, true);
     if (st != W4A8_OK) return st;
-    const long long n = (long long)T * (H / 8);
-    st = launch_maybe_pdl(combine_kernel, (unsigned)((n + 255) / 256), 256, s, true, yd, wts, inv, T, topk, H, out);
-    return st != W4A8_OK ? st : last_cuda();
+    return launch_combine(yd, wts, inv, T, topk, H, out, s, true);
 }
 
 }  // namespace
