@@ -73,6 +73,7 @@ struct W16GroupedParams {
 };
 
 constexpr int kW16GEpiWarp0 = 3;       // after the two producers and the MMA warp
+constexpr int kW16GXSeenWarp = 7;
 constexpr int kW16GDqWarp0 = 8;        // a multiple of 4: a warp's TMEM lanes follow from its number
 constexpr int kW16GKSW = 2;            // k-blocks of 64 per stage of packed weights: a unit's
 
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* w_full = bars;                   // [NW] codes, scales, zero-points landed
     uint64_t* w_empty = w_full + C::NW;        // [NW] a team read them
-    uint64_t* full = w_empty + C::NW;          // [NS] dequantized weights written by a team
+    uint64_t* full = w_empty + C::NW;          // [NS] dequantized weights written by a team, activations landed
     uint64_t* empty = full + C::NS;            // [NS] their MMAs completed
     uint64_t* x_full = empty + C::NS;          // [NX] activations landed
     uint64_t* x_empty = x_full + C::NX;        // [NX] their MMAs completed
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
             mbar_init(&w_empty[i], 4);
         }
         for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&full[i], 4);
+            mbar_init(&full[i], 4 + 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < C::NX; ++i) {
@@ -370,42 +371,49 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
         // instead of being moved there one by one.
         {
             const bool leader = elect_one();
-            Ring rc, rx;
-            uint32_t phases = 0u, seq = 0u;
+            Ring rc, rx, ra;
             bool ok = true;
             while (ok && walk.next(tile, u0, u1)) {
                 const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
                 const uint32_t idesc = idesc_bf16((gt.rows + 15) & ~15);
-                if (!warp_wait_bounded(&acc_empty[rc.idx], rc.phase ^ 1u, wc)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + rc.idx * BN;
                 const XPlan<BN> x(gt.rows);
-                int xu = 0;                          // the unit's place in its activation stage
-                for (int u = u0; u < u1; ++u, ++seq) {
-                    const int slot = seq % C::NS;
-                    if (xu == 0 && !warp_wait_bounded(&x_full[rx.idx], rx.phase, wc)) { ok = false; break; }
-                    if (!warp_wait_bounded(&full[slot], (phases >> slot) & 1u, wc)) { ok = false; break; }
-                    tc_fence_after();
-                    const bool last = xu == x.units - 1 || u == u1 - 1;
-                    if (leader) {
-                        const uint32_t st = smem_u32(smem + rx.idx * C::XSTAGE) + xu * 2 * x.kstride;
-                        const uint32_t a = tmem_base + C::A_COL0 + slot * 64;
-                        const uint64_t bdesc = umma_desc_kmajor(st, 128);
+                const uint32_t kstep = (uint32_t)x.kstride >> 4;     // in descriptor units
+                if (!warp_wait_bounded(&acc_empty[rc.idx], rc.phase ^ 1u, wc)) { ok = false; break; }
+                const uint32_t d_tmem = tmem_base + rc.idx * BN;
+                uint32_t more = 0u;                                  // 0: the tile's first MMA
+                int left = u1 - u0, kbs = KB - 2 * u0;
+                while (left > 0) {
+                    // one activation stage
+                    uint64_t bdesc = umma_desc_kmajor(smem_u32(smem + rx.idx * C::XSTAGE), 128);
+                    const int n = min(left, x.units);
+                    left -= n;
+                    for (int i = n; i > 0; --i) {
+                        ok = warp_wait_bounded(&full[ra.idx], ra.phase, wc);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+                            const uint32_t a = tmem_base + C::A_COL0 + ra.idx * 64;
+                            mma_bf16_tmem_a(d_tmem, a, bdesc, idesc, more);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_bf16_tmem_a(d_tmem, a + 8 * kk, bdesc + 2 * kk, idesc, (u > u0 || kk > 0) ? 1u : 0u);
-                        if (2 * u + 1 < KB) {
+                            for (int kk = 1; kk < 4; ++kk)
+                                mma_bf16_tmem_a(d_tmem, a + 8 * kk, bdesc + 2 * kk, idesc, 1u);
+                            if (kbs > 1) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_bf16_tmem_a(d_tmem, a + 32 + 8 * kk, bdesc + (x.kstride >> 4) + 2 * kk, idesc, 1u);
+                                for (int kk = 0; kk < 4; ++kk)
+                                    mma_bf16_tmem_a(d_tmem, a + 32 + 8 * kk, bdesc + kstep + 2 * kk, idesc, 1u);
+                            }
+                            tc_commit(&empty[ra.idx]);
                         }
-                        tc_commit(&empty[slot]);
-                        if (last) tc_commit(&x_empty[rx.idx]);
+                        __syncwarp();
+                        more = 1u;
+                        kbs -= 2;
+                        bdesc += 2 * kstep;
+                        ra.next(C::NS);
                     }
+                    if (!ok) break;
+                    if (leader) tc_commit(&x_empty[rx.idx]);
                     __syncwarp();
-                    phases ^= 1u << slot;
-                    xu = last ? 0 : xu + 1;
-                    if (last) rx.next(C::NX);
+                    rx.next(C::NX);
                 }
                 if (!ok) break;
                 if (leader) tc_commit(&acc_full[rc.idx]);
@@ -421,6 +429,27 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
                 (void)wait_bounded(drain, 0, wd);
             }
             __syncwarp();
+        }
+    } else if (warp == kW16GXSeenWarp) {
+        // ------------------------------------ activations seen to have landed --
+        // Counts them in at each unit's stage of weights, so that the MMA warp,
+        // whose pace is the kernel's, has one wait for a unit.
+        Ring rx, ra;
+        bool ok = true;
+        while (ok && walk.next(tile, u0, u1)) {
+            const GroupedTile gt(g, p.E, p.n_tiles, BN, tile);
+            const XPlan<BN> x(gt.rows);
+            for (int u = u0, xu = 0; u < u1; ++u) {
+                ok = (xu > 0 || warp_wait_bounded(&x_full[rx.idx], rx.phase, wc)) &&
+                     warp_wait_bounded(&empty[ra.idx], ra.phase ^ 1u, wc);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(&full[ra.idx]);
+                ra.next(C::NS);
+                if (++xu == x.units || u == u1 - 1) {
+                    xu = 0;
+                    rx.next(C::NX);
+                }
+            }
         }
     } else if (warp >= kW16GDqWarp0) {
         // ----------------------------------------------------- dequantize --

@@ -138,6 +138,35 @@ def test_layer_size_sampled_experts(m):
         at += n
 
 
+@pytest.mark.parametrize("K,N,group,sym", [(192, 2112, 64, False), (128, 2176, 128, True), (320, 2304, 64, True)])
+def test_many_tiles(m, K, N, group, sym):
+    """Enough tiles for 256 columns each; the last one of 64, 128 and 256."""
+    counts = [5000, 0, 3, 9000, 193, 2500, 40, 8100, 5900]
+    w, W = _weights(m, len(counts), K, N, group, sym, seed=K)
+    X = gen_linear(sum(counts), K, 64, seed=N).X
+    Y = m.w4a16_grouped_gemm(X.cuda(), _offsets(counts), w)
+    at = 0
+    for e, n in enumerate(counts):
+        pick = sorted(set(range(0, n, 97)) | set(range(max(n - 3, 0), n)))
+        if pick:
+            Ye, A = O.w4a16_gemm(bits(X[at:at + n][pick]), _dequant(W[e], group, sym))
+            check_bf16(bits(Y[at:at + n][pick]), Ye, A, rel=fp32_bound(K), what=f"expert {e}")
+        at += n
+
+
+def test_many_tiles_of_few_rows(m):
+    """256-column tiles of 16 rows: one row for each of 300 experts, wide N."""
+    E, K, N = 300, 64, 16064
+    w, W = _weights(m, 2, K, N, 64, True, seed=3)
+    pick = torch.arange(E) % 2
+    big = m.PackedWeight(packed=w.packed[pick].contiguous(), s_w=w.s_w[pick].contiguous(), z=None, desc=w.desc, experts=E)
+    X = gen_linear(E, K, 64, seed=5).X
+    Y = m.w4a16_grouped_gemm(X.cuda(), _offsets([1] * E), big)
+    for e in (0, 1):
+        Ye, A = O.w4a16_gemm(bits(X[e::2]), _dequant(W[e], 64, True))
+        check_bf16(bits(Y[e::2]), Ye, A, rel=fp32_bound(K), what=f"weight {e}")
+
+
 def test_strided_rows_and_outputs(m):
     for counts in ([20, 0, 29, 1], [2, 1, 0, 2]):
         R = sum(counts)
