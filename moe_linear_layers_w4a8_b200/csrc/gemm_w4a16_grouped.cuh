@@ -22,22 +22,27 @@
 //     column's 128 k and gives the stage of packed weights back as soon as the
 //     codes are in registers.  (16 warps with 64 k each: what an iteration
 //     spends beside the weights, 125 instructions to their 187, made it 222 us
-//     to 214; three and four teams: no faster, they hold the MMA warp up.)
+//     to 214.  Three teams need tiles of 144 rows: 195 to 201 us there, but 309
+//     to 286 for 24576 rows over 64 experts, K = 2048, N = 2816.)
 //   * Activations come in stages of their own, longer in k where the rows are
 //     few: two units of them on their way (the stages of the weights) left the
 //     pipeline without arithmetic at 180 us, these at 145.
+//   * The MMA warp's pace is the kernel's: of 1,030 cycles for a unit it waited
+//     250 on barriers that were complete and issued for 390, slowed by the
+//     dequantizing warps beside it.  So it has one wait for a unit (another
+//     warp sees the activations land: 210 -> 201 us), and descriptors advance
+//     by additions.  Testing the next stage ahead: 206.
 //   * The producers and the MMA warp run converged, one lane issuing: a lone
 //     lane moves every descriptor and address to uniform registers one by one,
 //     135 cycles for each MMA instead of 32, 300 for each copy (245 -> 224 us
 //     from the producers, 310 -> 270 from the MMAs).
-//   * Bound by the dequantization (22 instructions for 8 weights, 13 of them
-//     at half rate, 26 cycles measured alone) beside the MMA warp's waits and
-//     issue: a unit takes 1,030 cycles of a CTA, 560 + 690 of a team's two
-//     units' worth in arithmetic, 840 of the MMA warp's.  At 144 rows and more
-//     the activations' way from L2 takes as long (10 TB/s over the SMs).  A
-//     mask is an immediate and 2^23 a register; a second constant for the
-//     flipped bit cost each mask a move (424 -> 369 us, 24576 rows over 64
-//     experts, K = 2048, N = 2816).
+//   * The dequantization takes 22 instructions for 8 weights, 13 of them at
+//     half rate: 26 cycles measured alone, 94 of the 201 us.  A mask is an
+//     immediate and 2^23 a register; a second constant for the flipped bit
+//     cost each mask a move (424 -> 369 us, the 24576 rows).  At 144 rows and
+//     more the activations come at 47 bytes a cycle for each SM, the bound of
+//     that case.  (256 columns to a tile, which halves them, cost the MMA warp
+//     more than it saved: 328 us.)
 // Tried and taken out: a kernel on mma.sync whose lanes keep the weights they
 // dequantize; its fragment loads and group scales came to 1.5 instructions for
 // a weight more: 280 us.
@@ -119,7 +124,8 @@ struct W16GCfg {
     static constexpr int A_COL0 = 2 * BN;
     static constexpr uint32_t TMEM_COLS = A_COL0 + 64 * NS <= 256 ? 256 : A_COL0 + 64 * NS <= 512 ? 512 : 1024;
     static_assert(TMEM_COLS <= 512, "TMEM");
-    static constexpr int SPLIT_GAIN = 3 + BN / 64;         // stages of 128 k (a partial tile is BN / 2 KB)
+    // a part of a split tile, in units / 16: 0.3 + 0.05 for each row (four warps add the parts)
+    static constexpr int PART0 = 5, PART1 = 13;
     static constexpr int LB = 16;                        // tokens per epilogue batch
     static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128 || BN == 192, "BN");
     static_assert(W_S % 128 == 0 && W_STAGE % 128 == 0, "TMA destinations");
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const WaitCtx wc{abort_flag, p.status, wait_cycles_for_ns(p.wait_ns)};
-    GroupedWalk walk(g, p.E, p.n_tiles, p.units, p.split_tiles, C::SPLIT_GAIN);
+    GroupedWalk walk(g, p.E, p.n_tiles, p.units, p.split_tiles, grouped_part(C::PART0, C::PART1, BN, p.R, g.mt[p.E]));
     const int KB = p.KB;
     const int kb_shift = p.group == 128 ? 1 : 0;   // k-blocks of 64 per group: 1 << kb_shift
     long long tile;

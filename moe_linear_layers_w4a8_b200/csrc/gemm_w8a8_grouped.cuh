@@ -29,7 +29,7 @@
 //     that share a weight box run side by side.
 //   * Persistent.  Enough tiles: handed out round-robin.  Few tiles (a decode
 //     step of few experts): the (tile, k-block) units are cut into equal
-//     ranges, one for each CTA.  A CTA that holds part of a tile stores its
+//     ranges, at most one for each CTA.  A CTA that holds part of a tile stores its
 //     int32 partial tile and counts itself in; the one that completes the
 //     count adds all parts and writes the output.  Integer sums are exact in
 //     any order, so results do not depend on who comes last, and no CTA ever
@@ -96,7 +96,8 @@ struct W8GCfg {
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int ACC_COLS = 4 * BN;                 // two pairs of accumulators
     static constexpr uint32_t TMEM_COLS = ACC_COLS;
-    static constexpr int SPLIT_GAIN = 4 + BN / 16;          // k-blocks of 128 (a partial tile is BN KB)
+    // a part of a split tile, in k-blocks / 16: 0.8 + 0.027 for each row
+    static constexpr int PART0 = 13, PART1 = 7;
     static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128, "BN");
     static_assert(NST >= 3, "stages");
     static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -156,26 +157,57 @@ __device__ __forceinline__ void build_group_table(const GroupTable& g, const int
     __syncthreads();
 }
 
+// How `tiles` tiles of KB units go to `grid` CTAs: 0 for whole tiles in turn,
+// else the length of the equal ranges of units that the CTAs take.  cost: the
+// longest CTA's units x 16.  A range costs 2 units beside its own (two ends),
+// and each of a tile's parts `part` / 16 units when the CTA that comes last
+// adds them all (as written and read: 200 rows, K = N = 1024 in tiles of 128
+// rows, 8 parts each: 28.8 us, whole 9); so ranges longer than the shortest
+// ones, in fewer CTAs, are looked at too.
+// (T: 32 bits on the device, where every division counts: 64-bit ones put 0.7
+// us on a launch of 13.)
+template <typename T>
+__host__ __device__ inline int grouped_split(T tiles, T KB, T grid, T part, T& cost) {
+    const T first = (tiles * KB + grid - 1) / grid;
+    cost = (tiles + grid - 1) / grid * KB * 16;
+    T best = 0;
+    for (T q = first; q > 0 && (q == first || q < KB); q *= 2) {
+        const T parts = (KB + q - 1) / q;
+        const T c = 16 * q + 32 + (parts * q != KB ? parts + 1 : parts) * part;
+        if (c < cost) {
+            cost = c;
+            best = q;
+        }
+    }
+    return (int)best;
+}
+
+// The price of a tile's part (PART0 + PART1 / 16 for each of its rows), from
+// the mean rows of M tiles of at most bn.
+__host__ __device__ inline int grouped_part(int part0, int part1, int bn, unsigned R, unsigned M) {
+    const unsigned rows = M > 0 ? (R + M - 1) / M : 0;
+    return part0 + (int)(rows < (unsigned)bn ? rows : bn) * part1 / 16;
+}
+
 // A CTA's share of the work, as segments: k-blocks [kb0, kb1) of a tile.
 struct GroupedWalk {
     long long tiles, t;          // whole tiles: next tile (strided by the grid)
     int u, u1, Q, KB;            // split: unit range
     bool split;
 
-    // Split where that shortens the longest CTA's work by at least `gain` units:
-    // less does not pay for the partial tiles.
-    __device__ __forceinline__ GroupedWalk(const GroupTable& g, int E, int n_tiles, int KB_, int split_tiles, int gain) {
+    __device__ __forceinline__ GroupedWalk(const GroupTable& g, int E, int n_tiles, int KB_, int split_tiles, int part) {
         KB = KB_;
         tiles = (long long)g.mt[E] * n_tiles;
-        const long long grid = gridDim.x;
-        const long long waves = (tiles + grid - 1) / grid;
-        split = tiles < split_tiles && waves * KB - (tiles * KB + grid - 1) / grid >= gain;
         t = blockIdx.x;
         Q = 0;
         u = u1 = 0;
+        if (tiles < split_tiles) {
+            unsigned cost;
+            Q = grouped_split<unsigned>((unsigned)tiles, KB, gridDim.x, part, cost);
+        }
+        split = Q > 0;
         if (split) {
             const int U = (int)tiles * KB;  // below split_tiles * 2^10
-            Q = (U + (int)grid - 1) / (int)grid;
             u = min((int)blockIdx.x * Q, U);
             u1 = min(u + Q, U);
         }
@@ -291,7 +323,7 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const WaitCtx wc{abort_flag, p.status, wait_cycles_for_ns(p.wait_ns)};
-    GroupedWalk walk(g, p.E, p.n_tiles, p.KB, p.split_tiles, C::SPLIT_GAIN);
+    GroupedWalk walk(g, p.E, p.n_tiles, p.KB, p.split_tiles, grouped_part(C::PART0, C::PART1, BN, p.R, g.mt[p.E]));
     long long tile;
     int kb0, kb1;
 

@@ -525,37 +525,45 @@ struct W8GroupedPlan {
     size_t counts_off, ws_bytes;
 };
 
-// Tile height out of `sizes` (descending): the largest whose tiles should fill
-// the grid, taking min(E, R) + R / bn m-tiles for ragged rows, and whose next
-// smaller one is less than `tall` times the mean rows of an expert; where even
-// the smallest does not fill it, one that holds the mean rows (at most 64).
-int grouped_bn(long long R, int E, int n_tiles, int grid, const int* sizes, int n, int tall) {
-    const long long busy = std::max<long long>(1, std::min<long long>(E, R));
-    for (int i = 0; i < n; ++i)
-        if ((busy + R / sizes[i]) * n_tiles >= grid && (i == n - 1 || sizes[i + 1] * busy < tall * R)) return sizes[i];
-    const long long mean = (R + busy - 1) / busy;
-    for (int i = n - 1; i >= 0; --i)
-        if (sizes[i] >= mean || sizes[i] >= 64) return sizes[i];
-    return sizes[0];
+// m-tiles of bn rows to expect of R rows over `busy` experts: one for each
+// expert and more where they have more rows; uneven ones add some.
+long long grouped_m_tiles(long long R, long long busy, int bn) {
+    return std::max(busy + 3 * R / (10 * bn), R / bn + busy / 2);
 }
 
 W8GroupedPlan plan_w8_grouped(long long R, int E, int N, int K, bool gate_up, int sms) {
     W8GroupedPlan pl{};
-    const int cols = gate_up ? 128 : 256;
-    pl.n_tiles = (N + cols - 1) / cols;
     pl.KB = K / 128;
     pl.grid = sms <= 0 ? 1 : (sms > 254 ? 254 : sms);  // arrivals are counted in 8 bits
-    const int sizes[4] = {128, 64, 32, 16};
-    // Few rows: the smaller a tile, the deeper the ring of weight stages.  512
-    // rows over 32 uneven experts: 16, 32, 64, 128 rows 172, 164, 177, 175 us;
-    // 741 rows over 8 of 11, N = 1040: 11.8, 8.5, 9.5, 11.5 us.
-    pl.bn = grouped_bn(R, E, pl.n_tiles, pl.grid, sizes, 4, 2);
-    // Tiles of one 128-column box where even those fit the grid in one wave: no
-    // partial tiles to write and add (6 rows, K = 2048, N = 2816: 13.8 -> 12.0 us).
-    pl.halves = 2;
-    if (!gate_up && (std::min<long long>(E, R) + R / pl.bn) * ((N + 127) / 128) <= pl.grid) {
-        pl.halves = 1;
-        pl.n_tiles = (N + 127) / 128;
+    const long long busy = std::max<long long>(1, std::min<long long>(E, R));
+    // The tile height of the shortest estimated time, in SM cycles: a k-block
+    // of two boxes takes 600 cycles to load from L2 and 4 more for each row (a
+    // box alone 300), the last tile's drain 15 for each row, and the weights
+    // come from HBM once, a tenth slower where tall tiles leave a shorter ring
+    // of stages.  Measured at 16, 32, 64, 128 rows: 512 rows over 32 uneven
+    // experts, K = 7168, N = 4096 158, 154, 172, 170 us (32 taken); 741 over 8
+    // of 11, K = 1152, N = 1040 10.3, 8.0, 8.9, 10.8 (64); 1400 over 4, K =
+    // 1408, N = 384 13.8, 7.4, 8.0, 9.3 (32); 3000 over 3, K = N = 1024 19.7,
+    // 13.4, 11.8, 11.0 (128); 200 of one, K = N = 1024 6.4, 6.5, 7.1, 8.2 (16).
+    double least = 0.0;
+    for (int bn = 16; bn <= 128; bn *= 2) {
+        const long long m = grouped_m_tiles(R, busy, bn);
+        // Tiles of one 128-column box where even those fit the grid in one wave: no
+        // partial tiles to write and add (6 rows, K = 2048, N = 2816: 13.8 -> 12.0 us).
+        const int halves = !gate_up && m * ((N + 127) / 128) <= pl.grid ? 1 : 2;
+        const int cols = gate_up ? 128 : 128 * halves, n_tiles = (N + cols - 1) / cols;
+        long long cost;
+        grouped_split<long long>(m * n_tiles, pl.KB, pl.grid,
+                                 grouped_part(W8GCfg<16>::PART0, W8GCfg<16>::PART1, bn, (unsigned)R, (unsigned)m), cost);
+        const double work = cost / 16.0 * ((halves == 1 ? 300 : 600) + 4 * bn) + 15 * bn;
+        const double hbm = (double)busy * (gate_up ? 2 * N : N) * K / 3420 * (bn < 64 ? 1.0 : 1.1);
+        const double time = std::max(work, hbm) + 0.1 * work;
+        if (bn == 16 || time < least) {
+            least = time;
+            pl.bn = bn;
+            pl.halves = halves;
+            pl.n_tiles = n_tiles;
+        }
     }
     const long long fewest = ((R + pl.bn - 1) / pl.bn) * pl.n_tiles;
     if (pl.KB > 1 && fewest < 4LL * pl.grid) {
@@ -766,11 +774,27 @@ W8GroupedPlan plan_w16_grouped(long long R, int E, int N, int K, int sms) {
     pl.n_tiles = (N + 127) / 128;
     pl.KB = (K / 64 + 1) / 2;
     pl.grid = sms <= 0 ? 1 : (sms > 254 ? 254 : sms);
-    const int sizes[5] = {192, 128, 64, 32, 16};
-    // A taller tile dequantizes a weight fewer times.  512 rows over 32 uneven
-    // experts: 16, 64, 128, 192 rows 335, 247, 245, 224 us; 777 rows over 8 of
-    // 10, N = 1088: 29.4, 12.3, 13.4, 15.4 us; 6 experts of one row: 13.7 to 14.2.
-    pl.bn = grouped_bn(R, E, pl.n_tiles, pl.grid, sizes, 5, 16);
+    const long long busy = std::max<long long>(1, std::min<long long>(E, R));
+    // As above: a unit takes 950 cycles and 1.5 for each row, so a taller tile,
+    // which dequantizes a weight fewer times, pays soon.  Measured at 16, 64,
+    // 128, 192 rows: 512 rows over 32 uneven experts, K = 7168, N = 4096 327,
+    // 227, 219, 201 us (192 taken); 777 over 8 of 10, K = 1344, N = 1088 27.9,
+    // 12.7, 13.7, 15.0 (64); six experts of one row, K = 2048, N = 2816 13.2,
+    // 14.7, 14.6, 14.4 (16).
+    const int sizes[5] = {16, 32, 64, 128, 192};
+    double least = 0.0;
+    for (int bn : sizes) {
+        const long long m = grouped_m_tiles(R, busy, bn);
+        const double rows = (double)std::min<long long>(bn, (R + m - 1) / m);
+        long long cost;
+        grouped_split<long long>(m * pl.n_tiles, pl.KB, pl.grid,
+                                 grouped_part(W16GCfg<16>::PART0, W16GCfg<16>::PART1, bn, (unsigned)R, (unsigned)m), cost);
+        const double time = cost / 16.0 * (950 + 1.5 * rows) + 12 * rows + 2 * bn;
+        if (bn == 16 || time < least) {
+            least = time;
+            pl.bn = bn;
+        }
+    }
     const long long fewest = ((R + pl.bn - 1) / pl.bn) * pl.n_tiles;
     if (pl.KB > 1 && fewest < 16LL * pl.grid) {
         pl.split_tiles = 16 * pl.grid;
