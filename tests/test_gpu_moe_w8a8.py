@@ -87,7 +87,7 @@ def test_layer(m, T, E, topk, H, I, zipf):
 
 @pytest.mark.parametrize("R,E,I", [
     (1, 3, 128), (40, 3, 256), (130, 2, 384), (600, 4, 128),
-    (4, 1, 1024), (30, 1, 1152), (60, 1, 1280), (1200, 4, 1664),      # split along k, tiles of 16 to 128 rows
+    (4, 1, 1024), (40, 2, 2048), (1200, 20, 1024), (1200, 4, 1664),      # split along k, tiles of 16 to 128 rows
 ])
 def test_gate_up_stage(m, R, E, I):
     """w2 = the identity in codes of 127 and scales of 1/127, so that a row

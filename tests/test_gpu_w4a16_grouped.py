@@ -69,13 +69,20 @@ CASES = [
     ([24, 0, 1], 4096, 64, 128, True, 0, 0),
     ([30], 1024, 64, 128, True, 0, 0),
     ([30], 1088, 64, 64, False, 1, 0),
-    # 128-row tiles with every number of activation boxes, whole and split along k
-    ([1] * 26 + [60, 70, 40, 7], 256, 640, 128, True, 0, 3),
-    ([1] * 26 + [60, 70, 40, 7], 768, 640, 64, False, 0, 0),
-    # and 192-row tiles
+    # tiles of 32 to 192 rows, split along k or whole
+    ([192] * 12, 128, 64, 128, True, 0, 0),
+    ([4] * 40, 896, 64, 64, False, 0, 0),
+    ([192] * 24, 128, 64, 64, True, 0, 0),
+    ([10] * 12, 1024, 320, 128, False, 0, 1),
+    ([10] * 24, 128, 768, 128, False, 0, 0),
+    ([10] * 24, 1024, 320, 64, True, 0, 0),
+    ([20] * 24, 128, 768, 64, False, 1, 0),
+    ([20] * 24, 2048, 320, 128, True, 0, 0),
+    # with every number of activation boxes
+    ([384, 400, 380, 191, 192, 193, 97, 96, 500, 410, 1, 60, 30, 385, 380, 390], 320, 640, 64, False, 0, 2),
     ([193, 0, 192, 191, 97, 96, 65, 64, 33, 32, 1, 500, 10, 128, 2, 31], 320, 1280, 64, False, 2, 0),
-    ([193, 0, 192, 191, 97, 96, 65, 64, 33, 32, 1, 500, 10, 128, 2, 31], 1024, 1280, 128, True, 0, 0),
-    ([10] * 16, 896, 1280, 128, False, 0, 0),
+    ([193, 0, 192, 191, 97, 96, 65, 64, 33, 32, 1, 500, 10, 128, 2, 31] * 2, 192, 1280, 64, True, 0, 0),
+    ([193, 0, 192, 191, 97, 96, 65, 64, 33, 32, 1, 500, 10, 128, 2, 31], 2048, 640, 128, True, 0, 0),
 ]
 
 

@@ -53,16 +53,13 @@ CASES = [
     ([1] * 512, 128, 32, 0, 0),                        # the most experts
     ([5, 0, 90], 7168, 144, 0, 0),                     # long k, few tiles: split with many parts
     ([300, 20, 0, 700], 1408, 2048, 0, 0),
-    # one wave of 128-column tiles (the first two) and more than one, split along k
+    # tiles of 16 and 32 rows, one box of columns or two, split along k or whole
     ([4], 2048, 208, 0, 0),
-    ([60], 2048, 400, 0, 0),
     ([1] * 20, 896, 2304, 0, 0),
-    ([10] * 20, 1024, 2048, 0, 0),
-    ([20] * 16, 1280, 2560, 0, 0),
-    ([40] * 10, 1664, 3840, 0, 0),
-    # and whole
-    ([10] * 20, 128, 2048, 0, 0),
-    ([300, 20, 0, 700], 256, 3840, 3, 1),              # BN = 128
+    ([192] * 12, 128, 64, 0, 0),
+    ([40] * 20, 4096, 64, 1, 1),
+    ([4] * 16, 128, 2304, 0, 0),
+    ([100] * 40, 896, 192, 0, 0),
 ]
 
 
@@ -93,6 +90,25 @@ def test_grouped_gemm(m, counts, K, N, front, behind):
     out2 = torch.full_like(out, -7.0)
     m.w8a8_grouped_linear(inp.X.cuda()[:R], off, w, out=out2, status=st)
     assert m.w4a8_get_device_status(st) == 0 and torch.equal(out2, out)
+
+
+@pytest.mark.parametrize("counts,K,N", [
+    ([192] * 24, 128, 64), ([192] * 24, 2048, 64), ([60] * 40, 128, 320), ([192] * 24, 2048, 192),       # 64 rows
+    ([250] * 40, 256, 64), ([120] * 40, 256, 320), ([300, 20, 0, 700, 129] * 5, 256, 768), ([500] * 40, 1664, 128),   # 128
+])
+def test_taller_tiles_equal_the_dense_product(m, counts, K, N):
+    """Tiles of 64 and 128 rows, one box of columns or two, split along k or
+    whole: every expert's rows bit for bit as w8a8_gemm gives them."""
+    w = _weights(m, len(counts), K, N, seed=len(counts))
+    R = sum(counts)
+    X = torch.randn(R, K, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").bfloat16()
+    q, sx, _ = m.w4a8_quant_act(X)
+    Y = m.w8a8_grouped_gemm(q, sx, _offsets(counts), w)
+    at = 0
+    for e, n in enumerate(counts):
+        if n:
+            assert torch.equal(Y[at:at + n], m.w8a8_gemm(q[at:at + n].clone(), sx[at:at + n].clone(), _one(w, e, m)))
+        at += n
 
 
 def test_layer_size_sampled_experts(m):
