@@ -491,8 +491,8 @@ __global__ void __launch_bounds__(W16GCfg<BN>::THREADS, 1)
                     s0 = *reinterpret_cast<const float*>(st + C::W_S + r * 4);
                     if (!SYM) z0 = st[C::W_Z + r];
                     if (two) {
-                        c[2] = *reinterpret_cast<const uint4*>(st + off_c + 2048);
-                        c[3] = *reinterpret_cast<const uint4*>(st + off_c + 3072);
+                        c[2] = *reinterpret_cast<const uint4*>(st + off_c + 2 * 1024);
+                        c[3] = *reinterpret_cast<const uint4*>(st + off_c + 3 * 1024);
                         s1 = *reinterpret_cast<const float*>(st + C::W_S + (g1 * 128 + r) * 4);
                         if (!SYM) z1 = st[C::W_Z + g1 * 128 + r];
                     }

@@ -528,7 +528,7 @@ struct W8GroupedPlan {
 // m-tiles of bn rows to expect of R rows over `busy` experts: one for each
 // expert and more where they have more rows; uneven ones add some.
 long long grouped_m_tiles(long long R, long long busy, int bn) {
-    return std::max(busy + 3 * R / (10 * bn), R / bn + busy / 2);
+    return std::max(busy + 3 * R / (10 * bn), R / bn + 2 * busy / 5);
 }
 
 W8GroupedPlan plan_w8_grouped(long long R, int E, int N, int K, bool gate_up, int sms) {
