@@ -147,7 +147,7 @@ def test_layer_size_sampled_experts(m):
 
 @pytest.mark.parametrize("K,N,group,sym", [(192, 2112, 64, False), (128, 2176, 128, True), (320, 2304, 64, True)])
 def test_many_tiles(m, K, N, group, sym):
-    """Enough tiles for 256 columns each; the last one of 64, 128 and 256."""
+    """Many tiles for each CTA; the last columns half a box, an odd and an even number of boxes."""
     counts = [5000, 0, 3, 9000, 193, 2500, 40, 8100, 5900]
     w, W = _weights(m, len(counts), K, N, group, sym, seed=K)
     X = gen_linear(sum(counts), K, 64, seed=N).X
@@ -162,7 +162,7 @@ def test_many_tiles(m, K, N, group, sym):
 
 
 def test_many_tiles_of_few_rows(m):
-    """256-column tiles of 16 rows: one row for each of 300 experts, wide N."""
+    """Many tiles of 16 rows for each CTA: one row for each of 300 experts, wide N."""
     E, K, N = 300, 64, 16064
     w, W = _weights(m, 2, K, N, 64, True, seed=3)
     pick = torch.arange(E) % 2
