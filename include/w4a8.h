@@ -563,7 +563,9 @@ W4A8_API w4a8_status w4a8_moe_combine(const uint16_t* y_rows, const float* topk_
 /*
  * The MoE layer with W8A8 experts: w4a8_moe_grouped_gemm's seven steps with
  * INT8 expert weights (one scale for each output channel) in steps 4 and 6:
- *   gate_up  y = s_x (s_w acc), h = silu(gate) * up in fp32, stored as bf16;
+ *   gate_up  y = s_x (s_w acc), h = silu(gate) * up in fp32 (SiLU's power and
+ *            quotient within 2^-15 of their value, hardware approximations;
+ *            w4a8_moe_grouped_gemm rounds both correctly), stored as bf16;
  *   down     y = s_h (s_w acc), expert outputs stored as bf16.
  * w1_q int8 [E][2I][H], w1_s fp32 [E][2I] (gate = columns [0, I)); w2_q int8
  * [E][H][I], w2_s fp32 [E][H]: stacked w8a8_pack_weights results, w1 = {K = H,

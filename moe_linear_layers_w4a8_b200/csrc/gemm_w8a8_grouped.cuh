@@ -267,6 +267,19 @@ __device__ __forceinline__ int count_in(unsigned long long* word, unsigned long 
     }
 }
 
+// silu(y) = y / (1 + e^-y), as y e^y / (1 + e^y) for y < 0: the power never
+// overflows and the quotient's divisor stays in [1, 2], so gates below -87 keep
+// their value down to fp32's subnormals.  h's bf16 rounding is 2^-8; the power
+// is within 2^-17 (its argument's rounding, 2^-24 of up to 88, and ex2's 2^-22)
+// and the fast quotient within 2^-22.  With expf and the correctly rounded
+// quotient the epilogue, not the MMAs, set the pace (13,000 of 15,000 cycles a
+// tile at K = 2048).
+__device__ __forceinline__ float silu_fast(float y) {
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(-1.442695041f * fabsf(y)));
+    return __fdividef(y < 0.0f ? y * e : y, 1.0f + e);
+}
+
 template <int BN, bool GATEUP>
 __global__ void __launch_bounds__(kW8GThreads, 1)
     w8a8_grouped_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
@@ -536,10 +549,7 @@ __global__ void __launch_bounds__(kW8GThreads, 1)
                         float y = sx * (sw0 * (float)(int32_t)a[j]);
                         if constexpr (GATEUP) {
                             const float up = sx * (sw1 * (float)(int32_t)b[j]);
-                            // h's bf16 rounding is 2^-8: __expf and the fast quotient are within 2^-16 for
-                            // y > -87 and give 0 below, where silu is under 2e-36; with the exact ones this
-                            // epilogue, not the MMAs, set the pace (13,000 of 15,000 cycles a tile at K = 2048)
-                            y = __fdividef(y, 1.0f + __expf(-y)) * up;
+                            y = silu_fast(y) * up;
                         }
                         stg[j * 32 + lane] = f32_to_bf16_bits(y);
                     }
