@@ -543,6 +543,10 @@ W4A8_API w4a8_status w4a8_moe_experts(const uint16_t* X, const int32_t* expert_i
 /* Workspace bytes w4a8_moe_dispatch needs for P pairs. */
 W4A8_API size_t w4a8_moe_dispatch_workspace_size(int P, int E);
 
+/* Kernels that dispatch (step 2) launches for T tokens of topk pairs: 1 or 3
+ * (0 when T, E or topk is out of range).  For counting launches; host only. */
+W4A8_API int w4a8_moe_dispatch_launches(int T, int E, int topk);
+
 /* w4a8_moe_dispatch — step 2 alone: the order of P rows by expert, stable, for
  * the grouped products.  expert_ids device int32 [P] in [0, E) (others are
  * reported as W4A8_ERR_INVALID_ARG through dev_status and taken as 0);
@@ -565,7 +569,8 @@ W4A8_API w4a8_status w4a8_moe_combine(const uint16_t* y_rows, const float* topk_
  * INT8 expert weights (one scale for each output channel) in steps 4 and 6:
  *   gate_up  y = s_x (s_w acc), h = silu(gate) * up in fp32 (SiLU's power and
  *            quotient within 2^-15 of their value, hardware approximations;
- *            w4a8_moe_grouped_gemm rounds both correctly), stored as bf16;
+ *            w4a8_moe_grouped_gemm has expf and a rounded quotient), stored as
+ *            bf16;
  *   down     y = s_h (s_w acc), expert outputs stored as bf16.
  * w1_q int8 [E][2I][H], w1_s fp32 [E][2I] (gate = columns [0, I)); w2_q int8
  * [E][H][I], w2_s fp32 [E][H]: stacked w8a8_pack_weights results, w1 = {K = H,

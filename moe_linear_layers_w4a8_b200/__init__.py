@@ -27,7 +27,7 @@ __all__ = [
     "w4a16_gemm", "w4a16_gemm_workspace_size",
     "w8a8_pack_expert_weights", "w8a8_grouped_gemm", "w8a8_grouped_workspace_size", "w8a8_grouped_linear",
     "w8a8_grouped_linear_workspace_size", "w8a8_moe_grouped_gemm", "w8a8_moe_workspace_size", "w8a8_moe_experts",
-    "w4a8_moe_dispatch", "w4a16_grouped_gemm", "w4a16_grouped_workspace_size",
+    "w4a8_moe_dispatch", "w4a8_moe_dispatch_launches", "w4a16_grouped_gemm", "w4a16_grouped_workspace_size",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -176,6 +176,8 @@ def load_library():
         L.w4a16_grouped_workspace_size.argtypes = [I, I, D]
         L.w4a8_moe_dispatch_workspace_size.restype = S
         L.w4a8_moe_dispatch_workspace_size.argtypes = [I, I]
+        L.w4a8_moe_dispatch_launches.restype = I
+        L.w4a8_moe_dispatch_launches.argtypes = [I, I, I]
         L.w4a8_moe_dispatch.restype = st
         L.w4a8_moe_dispatch.argtypes = [P, I, I, P, P, P, P, S, P, P]
         L.w4a8_get_device_status.restype = st
@@ -634,6 +636,11 @@ def w4a8_moe_combine(y_rows: torch.Tensor, topk_w: torch.Tensor, out: Optional[t
         out = torch.empty(T, H, dtype=torch.bfloat16, device=y_rows.device)
     _check(L.w4a8_moe_combine(_p(y_rows), _p(topk_w), T, k, H, _p(out), _stream(y_rows.device)), "w4a8_moe_combine")
     return out
+
+
+def w4a8_moe_dispatch_launches(T: int, E: int, topk: int) -> int:
+    """Kernels that a layer's dispatch of T tokens launches (1 or 3; 0 out of range)."""
+    return int(load_library().w4a8_moe_dispatch_launches(int(T), int(E), int(topk)))
 
 
 def w4a8_moe_dispatch(expert_ids: torch.Tensor, E: int, status: Optional[torch.Tensor] = None):

@@ -464,9 +464,6 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const float* __restrict
 // the prefix over experts of ceil(count / BN) m-tiles for the grouped GEMMs.
 // ---------------------------------------------------------------------------
 constexpr int kDispatchThreads = 256;
-// Tokens up to which one CTA is faster than the three launches below (333
-// tokens, cold: 6.5 us to 4.1 + 3.8 + 4.5).
-constexpr int kDispatchOneCta = 512;
 constexpr int kMaxExperts = 512;
 
 __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const int32_t* __restrict__ idx, int T,

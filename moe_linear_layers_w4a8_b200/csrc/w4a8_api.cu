@@ -368,13 +368,25 @@ w4a8_status launch_route_quant(const float* logits, int T, int E, int topk, int3
     return last_cuda();
 }
 
+// Whether one CTA dispatches T tokens of topk pairs over E experts.  Its first
+// chunk of 256 tokens always pays; the pairs of a second one cost it more than
+// the three launches of many CTAs do once there are many, sooner with more
+// experts.  Layer time by one CTA / by three launches, us (small H and I): 64
+// experts 400 x 8 41.4 / 42.0, 512 x 8 43.6 / 43.2, 400 x 16 62.8 / 61.0, 512 x
+// 16 60.0 / 55.3; 256 experts 320 x 8 44.6 / 45.4, 400 x 8 46.4 / 46.3, 512 x 16
+// 68.6 / 62.9; 512 experts 320 x 3 44.9 / 45.9, 320 x 8 58.1 / 57.7, 512 x 16
+// 80.0 / 73.6; 13 experts 333 x 3, dispatch alone 6.5 / 12.4.
+bool dispatch_by_one_cta(int T, int E, int topk) {
+    return T <= kDispatchThreads || (T <= 2 * kDispatchThreads && (T - kDispatchThreads) * topk <= 1400 - 2 * E);
+}
+
 // Expert offsets, m-tile prefix for tiles of bn rows, and the permutation of
 // T * topk pairs, all ids already in [0, E).  dcnt: dispatch_ctas(T) * E ints.
 // pdl: chained to the preceding kernel by programmatic stream serialization.
 w4a8_status launch_dispatch(const int32_t* idx, int T, int E, int topk, int bn, int32_t* offsets, int32_t* mtile_off,
                             int32_t* perm, int32_t* inv, int32_t* dcnt, cudaStream_t s, bool pdl = false) {
     w4a8_status st;
-    if (T <= kDispatchOneCta) {
+    if (dispatch_by_one_cta(T, E, topk)) {
         st = launch_maybe_pdl(dispatch_kernel, 1, kDispatchThreads, s, pdl, idx, T, E, topk, bn, offsets, mtile_off,
                               perm, inv);
         return st != W4A8_OK ? st : last_cuda();
@@ -1486,6 +1498,11 @@ w4a8_status w8a8_moe_experts(const uint16_t* X, const int32_t* expert_ids, int R
     int32_t* offsets = reinterpret_cast<int32_t*>(wts + R);
     return moe_w8_impl(X, nullptr, expert_ids, R, E, 1, w1_q, w1_s, w1, w2_q, w2_s, w2, y_out, idx, wts, offsets, ws,
                        dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int w4a8_moe_dispatch_launches(int T, int E, int topk) {
+    if (T <= 0 || E <= 0 || E > kMaxExperts || topk <= 0 || topk > 16 || topk > E) return 0;
+    return dispatch_by_one_cta(T, E, topk) ? 1 : 3;
 }
 
 size_t w4a8_moe_dispatch_workspace_size(int P, int E) {
