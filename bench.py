@@ -330,9 +330,12 @@ class MoEWorkload:
         self.T, self.H, self.E, self.topk, self.I = c["T"], c["H"], c["E"], c["topk"], c["I"]
         self.group, self.sym, self.zipf, self.wp = c["group"], c["symmetric"], c["zipf"], c["w_outlier_p"]
         self.dev = device
-        # route, dispatch (one kernel, or count / scan / scatter above 256 tokens), quantize X,
-        # gate_up, quantize h, down, combine
-        self.launches_per_step = 7 + (2 if self.T > 256 else 0)
+
+    @property
+    def launches_per_step(self):
+        # route, dispatch (one kernel, or count / scan / scatter), quantize X, gate_up, quantize h, down, combine
+        import moe_linear_layers_w4a8_b200 as m
+        return 6 + m.w4a8_moe_dispatch_launches(self.T, self.E, self.topk)
 
     def _weight(self, e, which, device):
         from synth import gen_expert_weight

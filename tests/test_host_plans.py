@@ -21,3 +21,11 @@ def m():
 ])
 def test_dispatch_launches(m, T, E, topk, launches):
     assert m.w4a8_moe_dispatch_launches(T, E, topk) == launches
+
+
+@pytest.mark.parametrize("T,E,topk,launches", [(64, 256, 8, 7), (333, 13, 3, 7), (512, 512, 16, 9), (4096, 64, 6, 9)])
+def test_bench_counts_the_dispatch_launches(m, T, E, topk, launches):
+    import bench
+    wl = bench.MoEWorkload("moe_sym")
+    wl.T, wl.E, wl.topk = T, E, topk
+    assert wl.launches_per_step == launches
