@@ -768,8 +768,7 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_scatter_kernel(cons
 // Weighted combine ("Kimi 2.7 MoE, 4-bit storage to INT8" §4.3-4.4 step 5):
 // out[t] = sum_j p[t,j] * y[inv(t,j)], fp32 in slot order, one bf16 rounding.
 // One thread per (token, 8 consecutive columns): 16-byte loads and stores.  B
-// slots are loaded together: 8 for few tokens (latency: 5.0 -> 4.1 us for 333
-// x 1152), 4 for many (occupancy: 24.0 us to 26.8 for 4096 x 2048).
+// slots are loaded together, B = 1 one after the other (launch_combine says when).
 // ---------------------------------------------------------------------------
 template <int B>
 __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ Yd,
@@ -791,29 +790,43 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-    // B slots at a time: their positions, then their rows, each in one round trip
-    for (int j0 = 0; j0 < topk; j0 += B) {
-        int r[B];
-        float w[B];
-        uint4 v[B];
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const size_t at = (size_t)t * topk + min(j0 + i, topk - 1);
+    if constexpr (B == 1) {
+        for (int j = 0; j < topk; ++j) {
             // inv == null: the rows are already in (token, slot) order
-            r[i] = inv ? __ldg(inv + at) : (int)at;
-            w[i] = __ldg(p + at);
-        }
-#pragma unroll
-        for (int i = 0; i < B; ++i)
-            if (j0 + i < topk) v[i] = __ldg(reinterpret_cast<const uint4*>(Yd + (size_t)r[i] * H) + c);
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            if (j0 + i >= topk) break;
-            const uint32_t ws[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            const int r = inv ? __ldg(inv + (size_t)t * topk + j) : t * topk + j;
+            const float w = __ldg(p + (size_t)t * topk + j);
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(Yd + (size_t)r * H) + c);
+            const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint32_t bits = (e & 1) ? (ws[e >> 1] >> 16) : (ws[e >> 1] & 0xFFFFu);
-                acc[e] = fmaf(w[i], bf16_bits_to_f32(bits), acc[e]);
+                acc[e] = fmaf(w, bf16_bits_to_f32(bits), acc[e]);
+            }
+        }
+    } else {
+        // B slots at a time: their positions, then their rows, each in one round trip
+        for (int j0 = 0; j0 < topk; j0 += B) {
+            int r[B];
+            float w[B];
+            uint4 v[B];
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                const size_t at = (size_t)t * topk + min(j0 + i, topk - 1);
+                r[i] = inv ? __ldg(inv + at) : (int)at;
+                w[i] = __ldg(p + at);
+            }
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+                if (j0 + i < topk) v[i] = __ldg(reinterpret_cast<const uint4*>(Yd + (size_t)r[i] * H) + c);
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                if (j0 + i >= topk) break;
+                const uint32_t ws[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t bits = (e & 1) ? (ws[e >> 1] >> 16) : (ws[e >> 1] & 0xFFFFu);
+                    acc[e] = fmaf(w[i], bf16_bits_to_f32(bits), acc[e]);
+                }
             }
         }
     }

@@ -401,13 +401,30 @@ w4a8_status launch_dispatch(const int32_t* idx, int T, int E, int topk, int bn, 
     return st != W4A8_OK ? st : last_cuda();
 }
 
+// Slots that the combine loads together.  Grids of one wave (3 CTAs to an SM) are
+// bound by latency: 4 or 8 (us for 333 x 2048, top-3 2.6, one at a time 2.8;
+// 64 x 7168, top-8 2.9 to 3.7).  Larger ones hide it with CTAs, of which longer
+// batches leave fewer (1024 x 2048, top-6, one at a time 4.6, by 4 5.4; 4096 x
+// 7168, top-1, 25.9 and 35.5), until the rows come from HBM (three quarters of
+// L2's size and more: by 3 4096 x 2048, top-6 21.7, one at a time 24.3, by 4
+// 24.9; 4096 x 7168, top-8 83.8, 92.9, 91.4).
+int combine_batch(int T, int topk, int H) {
+    if (topk == 1) return 1;
+    const long long blocks = ((long long)T * (H / 8) + 255) / 256;
+    if (blocks <= 3 * 148) return topk <= 4 ? 4 : 8;
+    return topk > 2 && (long long)T * topk * H * 2 > 96000000ll ? 3 : 1;
+}
+
 // The weighted sum of a token's rows; inv == null: rows in (token, slot) order.
 w4a8_status launch_combine(const uint16_t* y, const float* w, const int32_t* inv, int T, int topk, int H, uint16_t* out,
                            cudaStream_t s, bool pdl = false) {
     const unsigned blocks = (unsigned)(((long long)T * (H / 8) + 255) / 256);
-    const w4a8_status st =
-        blocks <= 512 ? launch_maybe_pdl(combine_kernel<8>, blocks, 256, s, pdl, y, w, inv, T, topk, H, out)
-                      : launch_maybe_pdl(combine_kernel<4>, blocks, 256, s, pdl, y, w, inv, T, topk, H, out);
+    w4a8_status st = W4A8_ERR_UNSUPPORTED_SHAPE;
+    switch (combine_batch(T, topk, H)) {
+#define W4A8_COMBINE(n) case n: st = launch_maybe_pdl(combine_kernel<n>, blocks, 256, s, pdl, y, w, inv, T, topk, H, out); break;
+        W4A8_COMBINE(1) W4A8_COMBINE(3) W4A8_COMBINE(4) W4A8_COMBINE(8)
+#undef W4A8_COMBINE
+    }
     return st != W4A8_OK ? st : last_cuda();
 }
 
