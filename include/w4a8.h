@@ -422,6 +422,27 @@ W4A8_API w4a8_status w4a16_grouped_gemm(const uint16_t* X, int R, int ldx, const
                                         const w4a8_wdesc* w, uint16_t* Y, int ldy, void* workspace, size_t ws_bytes,
                                         int32_t* dev_status, void* stream);
 
+/* How a grouped product runs, for inspection (tests): its tiles and whether
+ * their units are split.  Host only; no GPU is needed when sms > 0. */
+typedef struct {
+    int64_t tiles;      /* row tiles of the given offsets x column tiles */
+    int32_t tile_rows;  /* rows of a tile at most */
+    int32_t tile_cols;  /* output columns of a tile */
+    int32_t units;      /* k-blocks of 128 to a tile */
+    int32_t ctas;
+    int32_t range;      /* 0: whole tiles in turn; else units (tile by tile, along k) to a CTA */
+} w4a8_grouped_plan;
+
+/* The plan of w8a8_grouped_gemm (gate_up != 0: of the layer's gate_up product,
+ * w = {K = H, N = 2I}) and of w4a16_grouped_gemm for R rows with these offsets
+ * (HOST memory, [E + 1], rising within [0, R]) on a GPU of `sms` SMs (0: the
+ * current device).  Errors: as the calls; INVALID_ARG for offsets that they
+ * would report. */
+W4A8_API w4a8_status w8a8_grouped_plan(int R, int E, const w4a8_wdesc* w, int gate_up, const int32_t* host_offsets,
+                                       int sms, w4a8_grouped_plan* out);
+W4A8_API w4a8_status w4a16_grouped_plan(int R, int E, const w4a8_wdesc* w, const int32_t* host_offsets, int sms,
+                                        w4a8_grouped_plan* out);
+
 /*
  * w4a8_moe_grouped_gemm — one MoE expert layer, following "Kimi 2.7 MoE,
  * 4-bit storage to INT8" §4.1-4.4:

@@ -28,6 +28,7 @@ __all__ = [
     "w8a8_pack_expert_weights", "w8a8_grouped_gemm", "w8a8_grouped_workspace_size", "w8a8_grouped_linear",
     "w8a8_grouped_linear_workspace_size", "w8a8_moe_grouped_gemm", "w8a8_moe_workspace_size", "w8a8_moe_experts",
     "w4a8_moe_dispatch", "w4a8_moe_dispatch_launches", "w4a16_grouped_gemm", "w4a16_grouped_workspace_size",
+    "w8a8_grouped_plan", "w4a16_grouped_plan",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -55,6 +56,11 @@ class WDesc(ctypes.Structure):
 
 class MoeWsLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in ("perm", "inv", "qx", "sx", "h", "qh", "sh", "yd", "total")]
+
+
+class GroupedPlan(ctypes.Structure):
+    _fields_ = [("tiles", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in
+                                              ("tile_rows", "tile_cols", "units", "ctas", "range")]
 
 
 @dataclasses.dataclass
@@ -174,6 +180,10 @@ def load_library():
         L.w4a16_grouped_gemm.argtypes = [P, I, I, P, I, P, P, P, D, P, I, P, S, P, P]
         L.w4a16_grouped_workspace_size.restype = S
         L.w4a16_grouped_workspace_size.argtypes = [I, I, D]
+        L.w8a8_grouped_plan.restype = st
+        L.w8a8_grouped_plan.argtypes = [I, I, D, I, P, I, ctypes.POINTER(GroupedPlan)]
+        L.w4a16_grouped_plan.restype = st
+        L.w4a16_grouped_plan.argtypes = [I, I, D, P, I, ctypes.POINTER(GroupedPlan)]
         L.w4a8_moe_dispatch_workspace_size.restype = S
         L.w4a8_moe_dispatch_workspace_size.argtypes = [I, I]
         L.w4a8_moe_dispatch_launches.restype = I
@@ -841,6 +851,28 @@ def w4a16_grouped_gemm(X: torch.Tensor, offsets: torch.Tensor, w: PackedWeight, 
     _launch(index, where, L.w4a16_grouped_gemm, X.data_ptr(), R, pitch, offsets.data_ptr(), E, packed.data_ptr(),
             s_w.data_ptr(), _addr(z), d, out.data_ptr(), ldy, *_scratch_args(ws), _addr(status))
     return out
+
+
+def _plan(where, fn, offsets, R, *args) -> dict:
+    host = [int(o) for o in offsets]
+    p = GroupedPlan()
+    _check(fn(host[-1] if R is None else int(R), len(host) - 1, *args[:-1], (ctypes.c_int32 * len(host))(*host),
+              args[-1], ctypes.byref(p)), where)
+    return {n: int(getattr(p, n)) for n, _ in GroupedPlan._fields_}
+
+
+def w8a8_grouped_plan(offsets, desc: WDesc, R: Optional[int] = None, gate_up: bool = False, sms: int = 0) -> dict:
+    """dict(tiles, tile_rows, tile_cols, units, ctas, range) of w8a8_grouped_gemm on
+    R rows (offsets[-1] when not given) with these host offsets (E + 1
+    integers); gate_up: of the layer's gate_up product.  sms: SMs of the GPU
+    (0: of the current device).  For inspection."""
+    return _plan("w8a8_grouped_plan", load_library().w8a8_grouped_plan, offsets, R, ctypes.byref(desc),
+                 int(bool(gate_up)), int(sms))
+
+
+def w4a16_grouped_plan(offsets, desc: WDesc, R: Optional[int] = None, sms: int = 0) -> dict:
+    """As w8a8_grouped_plan, of w4a16_grouped_gemm."""
+    return _plan("w4a16_grouped_plan", load_library().w4a16_grouped_plan, offsets, R, ctypes.byref(desc), int(sms))
 
 
 # ------------------------------------------------- MoE with INT8 experts ---

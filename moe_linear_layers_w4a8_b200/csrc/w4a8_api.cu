@@ -833,6 +833,25 @@ W8GroupedPlan plan_w16_grouped(long long R, int E, int N, int K, int sms) {
     return pl;
 }
 
+// What the CTAs of a grouped product derive from the offsets (build_group_table
+// and GroupedWalk), on the host.
+w4a8_status describe_plan(const W8GroupedPlan& pl, int part0, int part1, int tile_cols, int R, int E,
+                          const int32_t* offsets, w4a8_grouped_plan* out) {
+    if (!offsets || !out) return W4A8_ERR_INVALID_ARG;
+    long long m = 0;
+    for (int e = 0; e < E; ++e) {
+        const int32_t a = offsets[e], b = offsets[e + 1];
+        if (a < 0 || b < a || b > R) return W4A8_ERR_INVALID_ARG;
+        m += (b - a + pl.bn - 1) / pl.bn;
+    }
+    *out = w4a8_grouped_plan{m * pl.n_tiles, pl.bn, tile_cols, pl.KB, pl.grid, 0};
+    unsigned cost;
+    if (out->tiles < pl.split_tiles)
+        out->range = grouped_split<unsigned>((unsigned)out->tiles, pl.KB, pl.grid,
+                                             grouped_part(part0, part1, pl.bn, R, (unsigned)m), cost);
+    return W4A8_OK;
+}
+
 // The grouped W4A16 product.
 w4a8_status launch_w16_grouped(const uint16_t* X, int ldx, const int32_t* offsets, int R, int E,
                                const uint8_t* packed, const float* s_w, const uint8_t* z, const w4a8_wdesc* w,
@@ -1383,6 +1402,26 @@ w4a8_status w8a8_grouped_gemm(const int8_t* qx, const float* s_x, const int32_t*
     if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return W4A8_ERR_WORKSPACE;
     return launch_w8_grouped(qx, s_x, offsets, R, E, q_w, s_w, w->N, w->K, false, Y, ldy, workspace, dev_status,
                              static_cast<cudaStream_t>(stream), false);
+}
+
+w4a8_status w8a8_grouped_plan(int R, int E, const w4a8_wdesc* w, int gate_up, const int32_t* host_offsets, int sms,
+                              w4a8_grouped_plan* out) {
+    const w4a8_status st = check_w8_grouped(R, E, w);
+    if (st != W4A8_OK) return st;
+    if (sms < 0 || (gate_up && w->N % 2 != 0)) return W4A8_ERR_INVALID_ARG;
+    const W8GroupedPlan pl = plan_w8_grouped(R, E, gate_up ? w->N / 2 : w->N, w->K, gate_up != 0,
+                                             sms > 0 ? sms : sm_count_current());
+    return describe_plan(pl, W8GCfg<16>::PART0, W8GCfg<16>::PART1, gate_up ? 128 : 128 * pl.halves, R, E, host_offsets,
+                         out);
+}
+
+w4a8_status w4a16_grouped_plan(int R, int E, const w4a8_wdesc* w, const int32_t* host_offsets, int sms,
+                               w4a8_grouped_plan* out) {
+    const w4a8_status st = check_w16_grouped(R, E, w);
+    if (st != W4A8_OK) return st;
+    if (sms < 0) return W4A8_ERR_INVALID_ARG;
+    const W8GroupedPlan pl = plan_w16_grouped(R, E, w->N, w->K, sms > 0 ? sms : sm_count_current());
+    return describe_plan(pl, W16GCfg<16>::PART0, W16GCfg<16>::PART1, 128, R, E, host_offsets, out);
 }
 
 size_t w8a8_grouped_linear_workspace_size(int R, int E, const w4a8_wdesc* w) {
