@@ -59,7 +59,7 @@
 namespace w4a8 {
 
 struct W16GroupedParams {
-    int N, K, KB;                // KB = K / 64 k-blocks
+    int N, KB;                   // KB: k-blocks of 64
     int units;                   // stages of two k-blocks of a tile
     int E, R, G, group;
     int n_tiles;                 // ceil(N / 128)

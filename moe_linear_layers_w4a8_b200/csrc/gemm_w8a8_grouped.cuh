@@ -51,7 +51,7 @@ namespace w4a8 {
 
 struct W8GroupedParams {
     int N;                       // output columns (gate_up: I)
-    int K, KB;                   // KB = K / 128 k-blocks
+    int KB;                      // k-blocks of 128
     int E, R;
     int halves;                  // boxes of 128 columns to a tile: 2, plain and few tiles: 1
     int n_tiles;                 // ceil(N / (128 halves)), gate_up: ceil(I / 128)

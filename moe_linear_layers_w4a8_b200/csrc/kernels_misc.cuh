@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const float* __restrict
 // tokens are walked in chunks of 256; inside a chunk, a per-(warp, expert)
 // lane bitmask gives each pair its rank among earlier tokens.  Also writes
 // the prefix over experts of ceil(count / BN) m-tiles for the grouped GEMMs.
+// perm may be null (here and below): the INT8 layer needs only inv.
 // ---------------------------------------------------------------------------
 constexpr int kDispatchThreads = 256;
 constexpr int kMaxExperts = 512;
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const int32_
                 const int e = idx[(size_t)t * topk + j];
                 const int32_t pos = base[e] + wpre[warp][e] + __popc(bits[warp][e] & lt);
                 inv[(size_t)t * topk + j] = pos;
-                perm[pos] = t * topk + j;
+                if (perm) perm[pos] = t * topk + j;
             }
         }
         __syncthreads();
@@ -553,15 +554,15 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const int32_
 // each; a pair's rank among its expert's is counted over the earlier pairs;
 // the offsets are one warp's scan.  Then the CTA quantizes its token's row,
 // loaded meanwhile, into its positions.  Same outputs as route_topk_kernel,
-// dispatch_kernel and quant_act_kernel; K <= 8192.
+// dispatch_kernel (without the permutation) and quant_act_kernel; K <= 8192.
 constexpr int kRouteQuantTokens = 16;
 constexpr int kRouteQuantThreads = 32 * kRouteQuantTokens;
 
 template <int EPL>
 __global__ void __launch_bounds__(kRouteQuantThreads) route_quant_kernel(
     const float* __restrict__ logits, int T, int E, int topk, int32_t* __restrict__ idx, float* __restrict__ p,
-    int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ inv,
-    const uint16_t* __restrict__ X, int K, int8_t* __restrict__ q, float* __restrict__ s_x, int32_t* status) {
+    int32_t* __restrict__ offsets, int32_t* __restrict__ inv, const uint16_t* __restrict__ X, int K,
+    int8_t* __restrict__ q, float* __restrict__ s_x, int32_t* status) {
     constexpr int kPairs = kRouteQuantTokens * 16;
     __shared__ int32_t first[kMaxExperts];                         // counts, then first positions
     __shared__ int32_t expert[kPairs];
@@ -628,7 +629,6 @@ __global__ void __launch_bounds__(kRouteQuantThreads) route_quant_kernel(
         for (int k = 0; k < tid; ++k) pos += expert[k] == e;
         if (one) {
             inv[tid] = pos;
-            perm[pos] = tid;
         }
         const int j = tid - t * topk;
         if (j >= 0 && j < topk) place[j] = pos;
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_scatter_kernel(cons
                 const int e = idx[(size_t)t * topk + j];
                 const int32_t pos = base[e] + wpre[warp][e] + __popc(bits[warp][e] & lt);
                 inv[(size_t)t * topk + j] = pos;
-                perm[pos] = t * topk + j;
+                if (perm) perm[pos] = t * topk + j;
             }
         }
         __syncthreads();

@@ -355,10 +355,10 @@ w4a8_status launch_route(const float* logits, int T, int E, int topk, int32_t* i
 
 // Routing, dispatch and quantization of T <= kRouteQuantTokens tokens in one launch.
 w4a8_status launch_route_quant(const float* logits, int T, int E, int topk, int32_t* idx, float* w, int32_t* offsets,
-                               int32_t* perm, int32_t* inv, const uint16_t* X, int K, int8_t* q, float* s_x,
-                               int32_t* status, cudaStream_t s) {
+                               int32_t* inv, const uint16_t* X, int K, int8_t* q, float* s_x, int32_t* status,
+                               cudaStream_t s) {
     switch ((E + 31) / 32) {
-#define W4A8_ROUTE(n) case n: route_quant_kernel<n><<<(unsigned)T, kRouteQuantThreads, 0, s>>>(logits, T, E, topk, idx, w, offsets, perm, inv, X, K, q, s_x, status); break;
+#define W4A8_ROUTE(n) case n: route_quant_kernel<n><<<(unsigned)T, kRouteQuantThreads, 0, s>>>(logits, T, E, topk, idx, w, offsets, inv, X, K, q, s_x, status); break;
         W4A8_ROUTE(1) W4A8_ROUTE(2) W4A8_ROUTE(3) W4A8_ROUTE(4) W4A8_ROUTE(5) W4A8_ROUTE(6) W4A8_ROUTE(7)
         W4A8_ROUTE(8) W4A8_ROUTE(9) W4A8_ROUTE(10) W4A8_ROUTE(11) W4A8_ROUTE(12) W4A8_ROUTE(13)
         W4A8_ROUTE(14) W4A8_ROUTE(15) W4A8_ROUTE(16)
@@ -634,7 +634,6 @@ w4a8_status launch_w8_grouped(const int8_t* qx, const float* s_x, const int32_t*
         return W4A8_ERR_CUDA;
     W8GroupedParams p{};
     p.N = N;
-    p.K = K;
     p.KB = pl.KB;
     p.E = E;
     p.R = R;
@@ -873,7 +872,6 @@ w4a8_status launch_w16_grouped(const uint16_t* X, int ldx, const int32_t* offset
     }
     W16GroupedParams p{};
     p.N = w->N;
-    p.K = w->K;
     p.KB = w->K / 64;
     p.E = E;
     p.R = R;
@@ -1473,12 +1471,11 @@ w4a8_status moe_w8_impl(const uint16_t* X, const float* logits, const int32_t* p
     float* sh = reinterpret_cast<float*>(ws + L.base.sh);
     uint16_t* yd = reinterpret_cast<uint16_t*>(ws + L.base.yd);
     w4a8_status st;
-    int32_t* perm = reinterpret_cast<int32_t*>(ws + L.base.perm);
     // Every kernel waits for the one before it inside (programmatic
     // stream serialization), so that a launch's start-up overlaps that one's end.
     const bool fused = !pre_ids && T <= kRouteQuantTokens;
     if (fused) {
-        st = launch_route_quant(logits, T, E, topk, idx, wts, offsets, perm, inv, X, H, qx, sx, dev_status, s);
+        st = launch_route_quant(logits, T, E, topk, idx, wts, offsets, inv, X, H, qx, sx, dev_status, s);
         if (st != W4A8_OK) return st;
     } else {
         if (pre_ids) {
@@ -1488,8 +1485,8 @@ w4a8_status moe_w8_impl(const uint16_t* X, const float* logits, const int32_t* p
             st = launch_route(logits, T, E, topk, idx, wts, dev_status, s);
         }
         if (st != W4A8_OK) return st;
-        st = launch_dispatch(idx, T, E, topk, 128, offsets, reinterpret_cast<int32_t*>(ws + L.base.mtile_off), perm, inv,
-                             reinterpret_cast<int32_t*>(ws + L.base.dcnt), s, true);
+        st = launch_dispatch(idx, T, E, topk, 128, offsets, reinterpret_cast<int32_t*>(ws + L.base.mtile_off), nullptr,
+                             inv, reinterpret_cast<int32_t*>(ws + L.base.dcnt), s, true);
         if (st != W4A8_OK) return st;
         if ((st = launch_quant(X, T, H, H, qx, sx, nullptr, 0, inv, topk, dev_status, s, true)) != W4A8_OK) return st;
     }
