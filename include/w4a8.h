@@ -320,9 +320,11 @@ W4A8_API w4a8_status w8a8_linear(const uint16_t* X, int M, int ldx, const int8_t
  *            expert e (w4a8_moe_dispatch or w4a8_moe_grouped_gemm's
  *            expert_offsets_out).  An expert may have no rows.  Rows before
  *            offsets[0] and from offsets[E] on belong to nobody: they are
- *            neither read nor written.  Offsets that decrease or leave [0, R]
- *            are reported as W4A8_ERR_INVALID_ARG through dev_status; nothing
- *            outside [0, R) is accessed.
+ *            never used and never written, but may be loaded (a tile's box of
+ *            rows runs on past its expert's last), so they must not be
+ *            rewritten from another stream meanwhile.  Offsets that decrease or
+ *            leave [0, R] are reported as W4A8_ERR_INVALID_ARG through
+ *            dev_status; nothing outside [0, R) is accessed.
  *   q_w      int8 [E][N][K], s_w fp32 [E][N]: E stacked w8a8_pack_weights
  *            results; w describes one of them.
  *   Y[r,n] = s_x[r] * (s_w[e,n] * sum_k q_x[r,k] q_w[e,n,k])   (bf16 output)
@@ -355,8 +357,8 @@ W4A8_API size_t w8a8_grouped_linear_workspace_size(int R, int E, const w4a8_wdes
 
 /* w8a8_grouped_linear — per-token INT8 quantization of X bf16 [R][ldx] (as
  * w4a8_quant_act; X 16-byte aligned, ldx % 8 == 0) followed by
- * w8a8_grouped_gemm, in one call.  Rows that belong to nobody are not
- * quantized, so they may hold anything, NaN included. */
+ * w8a8_grouped_gemm, in one call.  Rows of X that belong to nobody are not
+ * read, so they may hold anything, NaN included. */
 W4A8_API w4a8_status w8a8_grouped_linear(const uint16_t* X, int R, int ldx, const int32_t* offsets, int E,
                                          const int8_t* q_w, const float* s_w, const w4a8_wdesc* w, uint16_t* Y,
                                          int ldy, void* workspace, size_t ws_bytes, int32_t* dev_status,
