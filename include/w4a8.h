@@ -543,7 +543,8 @@ W4A8_API w4a8_status w4a8_moe_debug_partials(
  */
 
 /* w4a8_moe_route — step 1 alone: topk_idx_out int32 [T][topk], topk_w_out
- * fp32 [T][topk] from logits fp32 [T][E] (device). */
+ * fp32 [T][topk] from logits fp32 [T][E] (device).  T <= 2^27, more is
+ * UNSUPPORTED_SHAPE. */
 W4A8_API w4a8_status w4a8_moe_route(const float* logits, int T, int E, int topk, int32_t* topk_idx_out,
                                     float* topk_w_out, int32_t* dev_status, void* stream);
 
@@ -581,7 +582,8 @@ W4A8_API w4a8_status w4a8_moe_dispatch(const int32_t* expert_ids, int P, int E, 
 
 /* w4a8_moe_combine — step 7 alone: out[t] = sum_j topk_w[t,j] * y_rows[t*topk
  * + j] in fp32, slot order, one bf16 rounding (y_rows bf16 [T*topk][H] in
- * (token, slot) order; H % 8 == 0; y_rows and out 16-byte aligned). */
+ * (token, slot) order; H % 8 == 0; y_rows and out 16-byte aligned).  T * topk <
+ * 2^31, more is UNSUPPORTED_SHAPE. */
 W4A8_API w4a8_status w4a8_moe_combine(const uint16_t* y_rows, const float* topk_w, int T, int topk, int H,
                                       uint16_t* out, void* stream);
 

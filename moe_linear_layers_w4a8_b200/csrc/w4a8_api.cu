@@ -1237,6 +1237,7 @@ w4a8_status w4a8_moe_grouped_gemm(const uint16_t* X, const float* logits, int T,
 w4a8_status w4a8_moe_route(const float* logits, int T, int E, int topk, int32_t* topk_idx_out, float* topk_w_out,
                            int32_t* dev_status, void* stream) {
     if (T < 0 || E <= 0 || topk <= 0 || topk > E || E > kMaxExperts || topk > 16) return W4A8_ERR_INVALID_ARG;
+    if (T > (1 << 27)) return W4A8_ERR_UNSUPPORTED_SHAPE;  // 32 threads for each, numbered in 32 bits
     if (T == 0) return W4A8_OK;
     if (!logits || !topk_idx_out || !topk_w_out) return W4A8_ERR_INVALID_ARG;
     return launch_route(logits, T, E, topk, topk_idx_out, topk_w_out, dev_status, static_cast<cudaStream_t>(stream));
@@ -1269,6 +1270,7 @@ w4a8_status w4a8_moe_experts(const uint16_t* X, const int32_t* expert_ids, int R
 w4a8_status w4a8_moe_combine(const uint16_t* y_rows, const float* topk_w, int T, int topk, int H, uint16_t* out,
                              void* stream) {
     if (T < 0 || topk <= 0 || H <= 0 || H % 8 != 0) return W4A8_ERR_INVALID_ARG;
+    if ((long long)T * topk >= (1ll << 31)) return W4A8_ERR_UNSUPPORTED_SHAPE;  // rows are numbered in 32 bits
     if (T == 0) return W4A8_OK;
     if (!y_rows || !topk_w || !out || !aligned16(y_rows) || !aligned16(out)) return W4A8_ERR_INVALID_ARG;
     return launch_combine(y_rows, topk_w, nullptr, T, topk, H, out, static_cast<cudaStream_t>(stream));

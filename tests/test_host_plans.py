@@ -76,3 +76,13 @@ def test_grouped_plan_refusals(m):
         m.w8a8_grouped_plan([0, 5], m.WDesc(8, 1, 256, 256, 64, 2), sms=148)
     assert e.value.code == 3
     assert m.w8a8_grouped_plan([0, 0], d8, R=0, sms=148)["tiles"] == 0
+
+
+def test_too_many_rows_are_refused(m):
+    """More (token, slot) rows than the kernels number in 32 bits: refused before
+    anything is launched (the pointers are never dereferenced)."""
+    lib, fake = m.load_library(), 256
+    for T, topk in [(1 << 27, 16), ((1 << 31) - 1, 2)]:
+        assert lib.w4a8_moe_combine(fake, fake, T, topk, 8, fake, None) == 2
+    for T in ((1 << 27) + 1, (1 << 31) - 1):
+        assert lib.w4a8_moe_route(fake, T, 16, 1, fake, fake, None, None) == 2
