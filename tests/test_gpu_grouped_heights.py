@@ -23,20 +23,21 @@ W8A8 = [
     ([1, 0, 15, 9], 128, 16, (16, 128, False)),
     ([0, 1], 2048, 16, (16, 128, True)),
     ([16, 15, 17] * 12, 128, 272, (16, 256, False)),
-    ([17, 17, 17, 1, 32, 17, 1, 32, 17, 16, 17, 15, 17, 3, 17, 9, 15, 17, 16, 17, 17, 0, 8, 1, 3, 32, 15, 32, 0, 32, 17,
-      1, 1, 16, 8, 3, 16], 896, 640, (16, 256, True)),
+    ([1, 17, 9, 17, 3, 9, 3, 0, 17, 16, 3, 17, 17, 9, 17, 15, 9, 8, 15, 3, 17, 17, 3, 17, 17, 1, 17, 16, 8, 0, 3], 896, 1024,
+     (16, 256, True)),
     ([32, 31, 33, 32] * 8, 128, 272, (32, 128, False)),
     ([33, 32, 31] * 8, 2048, 144, (32, 128, True)),
     ([32, 31, 33] * 12, 128, 272, (32, 256, False)),
-    ([33, 32, 31, 33, 33] * 7, 896, 640, (32, 256, True)),
+    ([32, 33, 31, 33, 32, 32, 33, 33, 33, 32, 32, 32, 33, 33, 33, 32, 32, 31, 33, 33, 32, 32, 31, 33, 33, 33, 31, 31, 33, 33,
+      32, 32, 31, 32, 32], 896, 640, (32, 256, True)),
     ([65, 64, 63, 64] * 8, 128, 272, (64, 128, False)),
     ([65, 63, 65, 65, 33, 32, 1, 33, 17, 33, 64, 32, 65, 128], 1152, 1024, (64, 128, True)),
     ([64, 65, 63] * 12, 128, 272, (64, 256, False)),
     ([65, 64, 65, 65, 65, 64, 65, 64, 64, 65, 64, 65, 65, 65, 63, 64, 65, 64, 65, 64, 63, 65, 65, 65, 64], 896, 1024,
      (64, 256, True)),
-    ([128, 127, 129, 128] * 8 + [128, 129, 64], 256, 272, (128, 128, False)),
+    ([128, 127, 129, 128] * 8 + [64, 65, 63], 384, 272, (128, 128, False)),
     ([1500, 300, 1500, 1500, 300, 128, 1000, 1, 1500, 1500, 65, 1], 7168, 16, (128, 128, True)),
-    ([128, 127, 129, 128] * 8 + [64, 65, 63], 256, 528, (128, 256, False)),
+    ([128, 127, 129, 128] * 9 + [64, 65, 63], 256, 272, (128, 256, False)),
     ([1, 127, 129, 65, 256, 256, 1, 1, 129, 64, 128, 3, 128, 129, 3, 127, 64, 3, 17, 65, 128, 129, 129, 127, 129, 1, 3, 17,
       128, 127, 64, 64, 128, 256, 127, 129, 65, 64, 17, 3], 2048, 640, (128, 256, True)),
 ]
@@ -45,7 +46,7 @@ GATE_UP = [
     ([1, 0, 17, 16], 128, 256, (16, 128, False)),
     ([1], 1152, 128, (16, 128, True)),
     ([32, 33, 31] * 7, 128, 384, (32, 128, False)),
-    ([33, 0, 33, 64, 1, 3, 17, 32, 33, 17, 32, 1], 2048, 128, (32, 128, True)),
+    ([16, 1, 17, 17, 3, 32, 64, 32, 1, 16, 0, 17, 17], 2048, 128, (32, 128, True)),
     ([65, 64, 63, 64] * 8 + [65, 64], 128, 256, (64, 128, False)),
     ([32, 63, 65, 3, 3, 3, 1, 3, 33, 3, 65, 17, 1, 64, 1, 128, 33, 63, 1, 65, 33, 128, 17, 128, 33], 896, 640,
      (64, 128, True)),
