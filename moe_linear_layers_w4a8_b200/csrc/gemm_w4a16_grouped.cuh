@@ -59,10 +59,11 @@
 namespace w4a8 {
 
 struct W16GroupedParams {
-    int N, KB;                   // KB: k-blocks of 64
+    int N;
     int units;                   // stages of two k-blocks of a tile
     int E, R, G, group;
     int n_tiles;                 // ceil(N / 128)
+    int KB;                      // k-blocks of 64
     const int32_t* offsets;      // [E + 1] device
     const uint8_t* packed;       // E stacked packed weights
     long long packed_estride;    // bytes between experts
