@@ -20,32 +20,23 @@
 //   * 8 warps dequantize, two teams of 4, units in turn, so that one team's
 //     waits and stores overlap the other's arithmetic.  A thread takes one
 //     column's 128 k and gives the stage of packed weights back as soon as the
-//     codes are in registers.  (16 warps with 64 k each: what an iteration
-//     spends beside the weights, 125 instructions to their 187, made it 222 us
-//     to 214.  Three teams need tiles of 144 rows: 195 to 201 us there, but 309
-//     to 286 for 24576 rows over 64 experts, K = 2048, N = 2816.)
+//     codes are in registers (16 warps with 64 k each: 222 us to 214).
 //   * Activations come in stages of their own, longer in k where the rows are
-//     few: two units of them on their way (the stages of the weights) left the
-//     pipeline without arithmetic at 180 us, these at 145.
-//   * The MMA warp's pace is the kernel's: of 1,030 cycles for a unit it waited
-//     250 on barriers that were complete and issued for 390, slowed by the
-//     dequantizing warps beside it.  So it has one wait for a unit (another
-//     warp sees the activations land: 210 -> 201 us), and descriptors advance
-//     by additions.  Testing the next stage ahead: 206.
+//     few: two units of them on their way left the pipeline without arithmetic
+//     at 180 us, these at 145.
+//   * The MMA warp's pace is the kernel's: of 1,030 cycles for a unit, whatever
+//     its rows, it waited 250 on barriers that were complete and issued for
+//     390, slowed by the dequantizing warps beside it.  So it has one wait for
+//     a unit (another warp sees the activations land: 210 -> 201 us), and
+//     descriptors advance by additions.
 //   * The producers and the MMA warp run converged, one lane issuing: a lone
 //     lane moves every descriptor and address to uniform registers one by one,
-//     135 cycles for each MMA instead of 32, 300 for each copy (245 -> 224 us
-//     from the producers, 310 -> 270 from the MMAs).
+//     135 cycles for each MMA instead of 32, 300 for each copy.
 //   * The dequantization takes 22 instructions for 8 weights, 13 of them at
 //     half rate: 26 cycles measured alone, 94 of the 201 us.  A mask is an
 //     immediate and 2^23 a register; a second constant for the flipped bit
-//     cost each mask a move (424 -> 369 us, the 24576 rows).  At 144 rows and
-//     more the activations come at 47 bytes a cycle for each SM, the bound of
-//     that case.  (256 columns to a tile, which halves them, cost the MMA warp
-//     more than it saved: 328 us.)
-// Tried and taken out: a kernel on mma.sync whose lanes keep the weights they
-// dequantize; its fragment loads and group scales came to 1.5 instructions for
-// a weight more: 280 us.
+//     would cost each mask a move.  At 144 rows and more the activations come at
+//     47 bytes a cycle for each SM, the bound of that case.
 #pragma once
 
 #include <cstdint>
