@@ -855,6 +855,8 @@ def w4a16_grouped_gemm(X: torch.Tensor, offsets: torch.Tensor, w: PackedWeight, 
 
 def _plan(where, fn, offsets, R, *args) -> dict:
     host = [int(o) for o in offsets]
+    if not host or not all(-2**31 <= v < 2**31 for v in (*host, 0 if R is None else int(R))):
+        _refuse(where, "offsets must be E + 1 integers, and like R of 32 bits")
     p = GroupedPlan()
     _check(fn(host[-1] if R is None else int(R), len(host) - 1, *args[:-1], (ctypes.c_int32 * len(host))(*host),
               args[-1], ctypes.byref(p)), where)

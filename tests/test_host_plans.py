@@ -68,7 +68,8 @@ def test_grouped_plan_refusals(m):
     for plan, d, wrong in ((m.w8a8_grouped_plan, d8, d4), (m.w4a16_grouped_plan, d4, d8)):
         for offsets, kw, desc, code in [([0, 5, 3], {}, d, 1), ([-1, 5], {}, d, 1), ([0, 5], dict(R=4), d, 1),
                                         ([0, 5], dict(sms=-1), d, 1), ([0], {}, d, 1), ([0, 5], {}, wrong, 3),
-                                        ([0] * 514, {}, d, 2), ([0, 5], dict(R=(1 << 24) + 1), d, 2)]:
+                                        ([0] * 514, {}, d, 2), ([], {}, d, 1), ([0, 2**32 + 5], {}, d, 1), ([0, 5], dict(R=2**32 + 5), d, 1),
+                                        ([0, 5], dict(R=(1 << 24) + 1), d, 2)]:
             with pytest.raises(m.W4A8Error) as e:
                 plan(offsets, desc, **{"sms": 148, **kw})
             assert e.value.code == code
